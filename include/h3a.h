@@ -280,6 +280,164 @@ h3a_status h3a_attention(const void* q, const void* k, const void* v, const h3a_
                          const int32_t* block_idx, int32_t k_blocks, int32_t block, float scale,
                          void* o, h3a_stream_t stream);
 
+/* ---- Prompt side: the conditioning text model's operators ------------------
+ * Rows are tokens of packed prompts (sequences behind one another, no
+ * padding); elements are bf16 or fp16, named by an h3a_dtype.  Pointers are
+ * 16-byte aligned and strides multiples of 8 elements unless said otherwise. */
+
+typedef enum { H3A_BF16 = 0, H3A_FP16 = 1 } h3a_dtype;
+
+/* A [tokens, heads, head_dim] tensor read and its counterpart written, both
+ * with head_dim contiguous and element strides of their own (a slice of a
+ * fused QKV buffer is one). */
+typedef struct {
+    int32_t heads, head_dim;
+    int64_t stride_n, stride_h;         /* of the input */
+    int64_t out_stride_n, out_stride_h; /* of the output */
+} h3a_heads_desc;
+
+#define H3A_ROPE_MAX_PAIRS 128
+
+/* Rotary frequencies of one model, made once on the host by
+ * h3a_rope_plan_scaled or h3a_rope_plan_from and passed to every h3a_rope
+ * call (read during the call only). */
+typedef struct {
+    int32_t pairs;                      /* rotated channels / 2 */
+    int32_t interleaved;                /* pair j is channels (2j, 2j+1), else (j, j + pairs) */
+    float amplitude;                    /* factor on the rotated channels */
+    int32_t reserved;
+    uint64_t turns[H3A_ROPE_MAX_PAIRS]; /* turns per position, modulo 1, in units of 2^-64 */
+} h3a_rope_plan;
+
+/* How h3a_rope_plan_scaled stretches theta^(-2j/rotary_dim) for contexts
+ * longer than the model was trained on, by `factor` s:
+ *   H3A_ROPE_PLAIN   not at all
+ *   H3A_ROPE_LINEAR  every frequency / s
+ *   H3A_ROPE_BASE    theta * s^(R / (R - 2)), R = rotary_dim: the slowest pair
+ *                    turns s times slower, the fastest as before
+ *   H3A_ROPE_PARTS   by n, the turns a pair makes over original_length: with
+ *                    w = clamp((n - low_turns) / (high_turns - low_turns), 0, 1)
+ *                    the frequency becomes f * (w + (1 - w) / s) */
+typedef enum { H3A_ROPE_PLAIN = 0, H3A_ROPE_LINEAR = 1, H3A_ROPE_BASE = 2, H3A_ROPE_PARTS = 3 } h3a_rope_scaling;
+
+/* Fills *plan.  Host only.  rotary_dim: even, 2 .. 256.  original_length,
+ * low_turns and high_turns are read for H3A_ROPE_PARTS only.
+ * Errors: INVALID_ARG for a null plan, an odd or non-positive rotary_dim,
+ * theta <= 0, factor <= 0, an unknown scaling, original_length < 1 or
+ * high_turns <= low_turns with H3A_ROPE_PARTS, or a value that is not finite;
+ * UNSUPPORTED for rotary_dim > 256. */
+h3a_status h3a_rope_plan_scaled(int32_t rotary_dim, int32_t interleaved, double theta, h3a_rope_scaling scaling,
+                                double factor, int64_t original_length, double low_turns, double high_turns,
+                                double amplitude, h3a_rope_plan* plan);
+
+/* Fills *plan from rotary_dim / 2 frequencies in radians per position (host
+ * array), for scalings the call above does not name.  Errors: as above. */
+h3a_status h3a_rope_plan_from(int32_t rotary_dim, int32_t interleaved, const double* frequencies, double amplitude,
+                              h3a_rope_plan* plan);
+
+/* One-dimensional rotary positions over q and, unless k is NULL, k.
+ * For every token n, head and pair j with channels (a, b):
+ *   angle = 2 pi * frac(positions[n] * turns[j])
+ *   a' = amplitude * (a cos - b sin), b' = amplitude * (a sin + b cos),
+ * with the angle negated when `inverse` is nonzero (which undoes a rotation of
+ * amplitude 1 and is the rotation's transpose); channels past the rotated ones
+ * pass through unchanged.  The angle's turn is exact for any int32 position
+ * (64-bit fixed point, modulo 1), cos and sin are fp32, one rounding to the
+ * element type.
+ * q, k        : device, layouts dq and dk; q_out and k_out: device.  An output
+ *               may be its own input with the same strides (in place) and must
+ *               not overlap anything else.
+ * positions   : device int32 [tokens], 4-byte aligned.
+ * Errors: INVALID_ARG for null or misaligned pointers, tokens < 0, heads < 1,
+ * head_dim < rotary_dim, head_dim or a stride no multiple of 8, a stride
+ * smaller than what it steps over or a plan not made by the calls above;
+ * UNSUPPORTED for head_dim > 512, tokens >= 2^31 or more than 65,535 heads in
+ * all. */
+h3a_status h3a_rope(const void* q, void* q_out, const h3a_heads_desc* dq, const void* k, void* k_out,
+                    const h3a_heads_desc* dk, h3a_dtype dtype, const int32_t* positions, int64_t tokens,
+                    const h3a_rope_plan* plan, int32_t inverse, h3a_stream_t stream);
+
+/* What h3a_residual_rmsnorm writes as y: the element type of x, or e4m3 (8
+ * bits) with one fp32 scale a row or a group of 128 channels. */
+typedef enum { H3A_SCALES_NONE = 0, H3A_SCALES_ROW = 1, H3A_SCALES_GROUP = 2 } h3a_scales;
+#define H3A_SCALE_GROUP 128
+
+/* The residual's addition and the root-mean-square norm, one pass over device
+ * memory (the prompt side's counterpart of h3a_residual_adaln).  For every row:
+ *   h = x + f, rounded once to the element type (f == NULL: h = x)
+ *   y = h / sqrt(mean(h^2) + eps) * gamma     (statistics of the rounded h, fp32)
+ * H3A_SCALES_NONE: y rounded once to the element type.  Otherwise, per row or
+ * per group of 128 channels (the last group may be shorter):
+ *   scale = max(max|y|, 2^-100) / 448, y8 = e4m3(y / scale) (nearest even),
+ * so that y8 * scale stands for y; a NaN makes its scale NaN.
+ * x, f, h_out : device, [rows, width] with row strides; f may be NULL.  h_out
+ *               is written when f != NULL (then required; may be x or f with
+ *               the same stride).
+ * gamma       : device fp32 [width].
+ * y_out       : device [rows, width] of the element type or of bytes, row
+ *               stride y_stride in its own elements; overlaps nothing else.
+ * scales_out  : device fp32 [rows] or [rows, ceil(width / 128)], 4-byte
+ *               aligned, NULL with H3A_SCALES_NONE.
+ * Errors: INVALID_ARG for null or misaligned pointers, rows < 0, width or a
+ * stride no positive multiple of 8, a stride below width, eps < 0 or NaN, an
+ * unknown dtype or scales; UNSUPPORTED for width > 16384 or rows >= 2^31. */
+h3a_status h3a_residual_rmsnorm(const void* x, int64_t x_stride, const void* f, int64_t f_stride, const float* gamma,
+                                int64_t rows, int32_t width, h3a_dtype dtype, float eps, h3a_scales scales,
+                                void* h_out, int64_t h_stride, void* y_out, int64_t y_stride, float* scales_out,
+                                h3a_stream_t stream);
+
+/* Shapes of one h3a_packed_attention call.  q and o are [total_q, heads,
+ * head_dim], k and v [total_k, kv_heads, head_dim], head_dim contiguous. */
+typedef struct {
+    h3a_dtype dtype;
+    int32_t seqs, heads, kv_heads, head_dim;
+    int64_t total_q, total_k;           /* rows of the tensors */
+    int64_t max_q, max_k;               /* no sequence has more queries / keys (max_k: see below) */
+    int64_t q_stride_n, q_stride_h, k_stride_n, k_stride_h, v_stride_n, v_stride_h, o_stride_n, o_stride_h;
+    int32_t causal;
+    float scale;                        /* logit scale; 0 selects 1 / sqrt(head_dim) */
+} h3a_packed_desc;
+
+/* Bytes of device workspace h3a_packed_attention needs for this descriptor: 0
+ * when no sequence's keys are split, else one fp32 partial row and its
+ * log-sum-exp per (split, query, head). */
+h3a_status h3a_packed_attention_workspace_size(const h3a_packed_desc* d, size_t* bytes);
+
+/* Attention over packed sequences with grouped heads, causal or not: whole
+ * prompts, pieces of prompts behind cached ones and single tokens over caches.
+ * Sequence s has the queries starts_q[s] .. starts_q[s+1]-1 and the keys
+ * starts_k[s] .. starts_k[s]+lk-1 with lk = lengths_k[s], or starts_k[s+1] -
+ * starts_k[s] when lengths_k is NULL (with lengths_k, a cache of fixed capacity
+ * per sequence, rows behind lk are never used).  Head h reads kv head
+ * h / (heads / kv_heads).  Query i of lq attends key j < lk, and when causal
+ * only j <= i + lk - lq (the last query sees every key):
+ *   o_i = sum_j softmax_j(scale * q_i . k_j) v_j,  lse_i = ln sum_j exp(scale * q_i . k_j)
+ * A query without keys (lk = 0, or causal and i + lk < lq) gets o = 0 and
+ * lse = -inf.  What a query does not attend has no influence on it, NaN and
+ * infinities included.  Rows of o and lse outside every sequence are left as
+ * they were.
+ * starts_q, starts_k: device int32 [seqs + 1], ascending; lengths_k: device
+ * int32 [seqs] or NULL.  Values that do not fit total_q / total_k are cut to
+ * them (no access outside the tensors).
+ * max_q bounds the sequences' queries (rows past it are left as they were);
+ * max_k only sizes the splits, so a wrong one costs time, not correctness.
+ * lse       : device fp32 [total_q, heads], contiguous, or NULL.
+ * workspace : device, h3a_packed_attention_workspace_size bytes, 16-byte
+ *             aligned; NULL when that is 0.  Calls that may overlap on the GPU
+ *             need workspaces of their own.
+ * QK^T and PV run on the tensor cores with fp32 accumulation; logits, maxima
+ * and sums are fp32; P is rounded to the element type for PV; o is rounded
+ * once.
+ * Errors: INVALID_ARG for null or misaligned pointers, seqs < 1, heads no
+ * positive multiple of kv_heads, negative sizes, max_q or max_k < 0, a stride no
+ * multiple of 8 or smaller than what it steps over, an unknown dtype, a scale
+ * that is negative or not finite; UNSUPPORTED for head_dim other than 64 / 96 /
+ * 128, more than 128 heads to a kv head, total_q or total_k >= 2^31, or a grid
+ * beyond 2^31 blocks; WORKSPACE if it is null, misaligned or too small. */
+h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, const h3a_packed_desc* d,
+                                const int32_t* starts_q, const int32_t* starts_k, const int32_t* lengths_k, void* o,
+                                float* lse, void* workspace, size_t ws_bytes, h3a_stream_t stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char* h3a_status_string(h3a_status s);
 

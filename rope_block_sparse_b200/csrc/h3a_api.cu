@@ -13,6 +13,7 @@
 
 #include "h3a.h"
 #include "h3a_internal.h"
+#include "prompt_internal.h"
 
 // Sticky per-device status word: kernels OR error bits into it.
 __device__ int g_h3a_status_word;
@@ -177,6 +178,54 @@ h3a_status prologue_check(const void* q, const void* k, const h3a_qkv_desc* d, c
     if (grid.T < 1 || grid.H < 1 || grid.W < 1) return H3A_ERR_INVALID_ARG;
     if (static_cast<int64_t>(grid.T) * grid.H * grid.W != d->N) return H3A_ERR_INVALID_ARG;
     if (!(eps >= 0.0f) || !(theta > 0.0)) return H3A_ERR_INVALID_ARG;
+    return H3A_OK;
+}
+
+bool known(h3a_dtype t) { return t == H3A_BF16 || t == H3A_FP16; }
+
+// Strides of a [rows, heads, d] tensor: multiples of 8 elements that step over
+// what lies inside them.  A dimension of size one is not stepped: any stride.
+bool strides_ok(int64_t sn, int64_t sh, int64_t rows, int64_t heads, int64_t d) {
+    return (heads <= 1 || (sh >= d && sh % 8 == 0)) && (rows <= 1 || (sn >= d && sn % 8 == 0));
+}
+
+h3a_status rope_plan_check(int32_t rotary_dim, const h3a_rope_plan* plan, double amplitude) {
+    if (!plan || rotary_dim < 2 || rotary_dim % 2 || !std::isfinite(amplitude)) return H3A_ERR_INVALID_ARG;
+    return rotary_dim > 2 * H3A_ROPE_MAX_PAIRS ? H3A_ERR_UNSUPPORTED : H3A_OK;
+}
+
+// Radians per position as a 64-bit fraction of a turn, modulo 1.
+uint64_t turns_of(double frequency) {
+    const double turns = frequency / 6.283185307179586476925;
+    const double part = turns - std::floor(turns);  // exact: [0, 1]
+    return static_cast<uint64_t>(std::fmod(std::ldexp(part, 64), 18446744073709551616.0));
+}
+
+// Checks a packed descriptor and lays out its partial rows.
+h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, size_t* rows_bytes, size_t* bytes) {
+    if (d == nullptr || !known(d->dtype)) return H3A_ERR_INVALID_ARG;
+    if (d->seqs < 1 || d->heads < 1 || d->kv_heads < 1 || d->heads % d->kv_heads) return H3A_ERR_INVALID_ARG;
+    if (d->total_q < 0 || d->total_k < 0 || d->max_q < 0 || d->max_k < 0) return H3A_ERR_INVALID_ARG;
+    if (!(d->scale >= 0.0f) || !std::isfinite(d->scale)) return H3A_ERR_INVALID_ARG;
+    if (d->head_dim != 64 && d->head_dim != 96 && d->head_dim != 128) return H3A_ERR_UNSUPPORTED;
+    if (d->heads / d->kv_heads > 128) return H3A_ERR_UNSUPPORTED;
+    const int64_t lim = int64_t(1) << 31;
+    if (d->total_q >= lim || d->total_k >= lim) return H3A_ERR_UNSUPPORTED;
+    if (!strides_ok(d->q_stride_n, d->q_stride_h, d->total_q, d->heads, d->head_dim) ||
+        !strides_ok(d->k_stride_n, d->k_stride_h, d->total_k, d->kv_heads, d->head_dim) ||
+        !strides_ok(d->v_stride_n, d->v_stride_h, d->total_k, d->kv_heads, d->head_dim) ||
+        !strides_ok(d->o_stride_n, d->o_stride_h, d->total_q, d->heads, d->head_dim))
+        return H3A_ERR_INVALID_ARG;
+    *plan = packed_plan(*d);
+    const double grid = static_cast<double>(d->seqs) * d->kv_heads * plan->row_blocks * plan->splits;
+    const double rows = static_cast<double>(d->total_q) * d->heads;
+    if (grid >= static_cast<double>(lim) || rows >= 4.0 * static_cast<double>(lim)) return H3A_ERR_UNSUPPORTED;
+    *rows_bytes = *bytes = 0;
+    if (plan->splits > 1) {
+        const size_t parts = static_cast<size_t>(plan->splits) * static_cast<size_t>(d->total_q) * d->heads;
+        *rows_bytes = align256(parts * d->head_dim * sizeof(float));
+        *bytes = *rows_bytes + align256(parts * sizeof(float));
+    }
     return H3A_OK;
 }
 
@@ -375,6 +424,145 @@ h3a_status h3a_residual_diff(const void* cur, const void* prev, int64_t n, doubl
         return H3A_ERR_WORKSPACE;
     cudaError_t e = launch_residual_diff(cur, prev, n, threshold, workspace, rel_out, reuse_out,
                                          reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? H3A_OK : cuda_fail(e);
+}
+
+h3a_status h3a_rope_plan_from(int32_t rotary_dim, int32_t interleaved, const double* frequencies, double amplitude,
+                              h3a_rope_plan* plan) {
+    const h3a_status rc = rope_plan_check(rotary_dim, plan, amplitude);
+    if (rc != H3A_OK) return rc;
+    if (!frequencies) return H3A_ERR_INVALID_ARG;
+    for (int j = 0; j < rotary_dim / 2; ++j)
+        if (!std::isfinite(frequencies[j])) return H3A_ERR_INVALID_ARG;
+    std::memset(plan, 0, sizeof(*plan));
+    plan->pairs = rotary_dim / 2;
+    plan->interleaved = interleaved ? 1 : 0;
+    plan->amplitude = static_cast<float>(amplitude);
+    for (int j = 0; j < plan->pairs; ++j) plan->turns[j] = turns_of(frequencies[j]);
+    return H3A_OK;
+}
+
+h3a_status h3a_rope_plan_scaled(int32_t rotary_dim, int32_t interleaved, double theta, h3a_rope_scaling scaling,
+                                double factor, int64_t original_length, double low_turns, double high_turns,
+                                double amplitude, h3a_rope_plan* plan) {
+    const h3a_status rc = rope_plan_check(rotary_dim, plan, amplitude);
+    if (rc != H3A_OK) return rc;
+    if (!(theta > 0.0) || !std::isfinite(theta) || !(factor > 0.0) || !std::isfinite(factor))
+        return H3A_ERR_INVALID_ARG;
+    if (scaling < H3A_ROPE_PLAIN || scaling > H3A_ROPE_PARTS) return H3A_ERR_INVALID_ARG;
+    if (scaling == H3A_ROPE_PARTS &&
+        (original_length < 1 || !std::isfinite(low_turns) || !std::isfinite(high_turns) || !(high_turns > low_turns)))
+        return H3A_ERR_INVALID_ARG;
+    const double r = rotary_dim;
+    if (scaling == H3A_ROPE_BASE && rotary_dim > 2) theta *= std::pow(factor, r / (r - 2.0));
+    double f[H3A_ROPE_MAX_PAIRS];
+    for (int j = 0; j < rotary_dim / 2; ++j) {
+        f[j] = std::pow(theta, -2.0 * j / r);
+        if (scaling == H3A_ROPE_LINEAR) f[j] /= factor;
+        if (scaling == H3A_ROPE_PARTS) {
+            const double n = static_cast<double>(original_length) * f[j] / 6.283185307179586476925;
+            const double w = std::fmin(std::fmax((n - low_turns) / (high_turns - low_turns), 0.0), 1.0);
+            f[j] *= w + (1.0 - w) / factor;
+        }
+    }
+    return h3a_rope_plan_from(rotary_dim, interleaved, f, amplitude, plan);
+}
+
+h3a_status h3a_rope(const void* q, void* q_out, const h3a_heads_desc* dq, const void* k, void* k_out,
+                    const h3a_heads_desc* dk, h3a_dtype dtype, const int32_t* positions, int64_t tokens,
+                    const h3a_rope_plan* plan, int32_t inverse, h3a_stream_t stream) {
+    if (!dq || !plan || !known(dtype) || tokens < 0 || (k && !dk)) return H3A_ERR_INVALID_ARG;
+    if (plan->pairs < 1 || plan->pairs > H3A_ROPE_MAX_PAIRS) return H3A_ERR_INVALID_ARG;
+    const int sides = k ? 2 : 1;
+    int64_t heads = 0;
+    RopeSide side[2] = {};
+    for (int i = 0; i < sides; ++i) {
+        const h3a_heads_desc& d = i ? *dk : *dq;
+        const void* x = i ? k : q;
+        void* y = i ? k_out : q_out;
+        if (d.heads < 1 || d.head_dim < 2 * plan->pairs || d.head_dim % 8 || d.head_dim != dq->head_dim)
+            return H3A_ERR_INVALID_ARG;
+        if (!strides_ok(d.stride_n, d.stride_h, tokens, d.heads, d.head_dim) ||
+            !strides_ok(d.out_stride_n, d.out_stride_h, tokens, d.heads, d.head_dim))
+            return H3A_ERR_INVALID_ARG;
+        if (tokens > 0 && (!x || !y)) return H3A_ERR_INVALID_ARG;
+        if (!aligned16(x) || !aligned16(y)) return H3A_ERR_INVALID_ARG;
+        if (x == y && (d.stride_n != d.out_stride_n || d.stride_h != d.out_stride_h)) return H3A_ERR_INVALID_ARG;
+        side[i] = RopeSide{x, y, d.stride_n, d.stride_h, d.out_stride_n, d.out_stride_h, d.heads};
+        heads += d.heads;
+    }
+    if (dq->head_dim > 512 || tokens >= (int64_t(1) << 31) || heads > 65535) return H3A_ERR_UNSUPPORTED;
+    if (tokens == 0) return H3A_OK;
+    if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u)) return H3A_ERR_INVALID_ARG;
+    cudaError_t e = launch_rope(side[0], side[1], dq->head_dim, dtype == H3A_FP16, positions, tokens, *plan, inverse != 0,
+                                reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? H3A_OK : cuda_fail(e);
+}
+
+h3a_status h3a_residual_rmsnorm(const void* x, int64_t x_stride, const void* f, int64_t f_stride, const float* gamma,
+                                int64_t rows, int32_t width, h3a_dtype dtype, float eps, h3a_scales scales,
+                                void* h_out, int64_t h_stride, void* y_out, int64_t y_stride, float* scales_out,
+                                h3a_stream_t stream) {
+    if (rows < 0 || width < 8 || width % 8 || !known(dtype) || !(eps >= 0.0f)) return H3A_ERR_INVALID_ARG;
+    if (scales < H3A_SCALES_NONE || scales > H3A_SCALES_GROUP) return H3A_ERR_INVALID_ARG;
+    auto stride_ok = [&](int64_t s) { return s % 8 == 0 && s >= width; };
+    if (!stride_ok(x_stride) || !stride_ok(y_stride) || (f && (!stride_ok(f_stride) || !stride_ok(h_stride))))
+        return H3A_ERR_INVALID_ARG;
+    if (width > kRmsNormMaxWidth || rows >= (int64_t(1) << 31)) return H3A_ERR_UNSUPPORTED;
+    if (rows == 0) return H3A_OK;
+    if (!x || !gamma || !y_out || (f && !h_out)) return H3A_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(gamma) || !aligned16(y_out) || (f && (!aligned16(f) || !aligned16(h_out))))
+        return H3A_ERR_INVALID_ARG;
+    if (f && ((h_out == x && h_stride != x_stride) || (h_out == f && h_stride != f_stride))) return H3A_ERR_INVALID_ARG;
+    if (scales != H3A_SCALES_NONE && (!scales_out || (reinterpret_cast<uintptr_t>(scales_out) & 3u)))
+        return H3A_ERR_INVALID_ARG;
+    const RmsNormArgs a{x, f, gamma, f ? h_out : nullptr, y_out, scales_out, x_stride, f_stride, h_stride, y_stride, rows, width, eps};
+    cudaError_t e = launch_residual_rmsnorm(a, dtype == H3A_FP16, scales, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? H3A_OK : cuda_fail(e);
+}
+
+h3a_status h3a_packed_attention_workspace_size(const h3a_packed_desc* d, size_t* bytes) {
+    PackedPlan plan;
+    size_t rows_bytes, all;
+    const h3a_status rc = packed_check(d, &plan, &rows_bytes, &all);
+    if (rc != H3A_OK) return rc;
+    if (bytes == nullptr) return H3A_ERR_INVALID_ARG;
+    *bytes = all;
+    return H3A_OK;
+}
+
+h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, const h3a_packed_desc* d,
+                                const int32_t* starts_q, const int32_t* starts_k, const int32_t* lengths_k, void* o,
+                                float* lse, void* workspace, size_t ws_bytes, h3a_stream_t stream) {
+    PackedPlan plan;
+    size_t rows_bytes, bytes;
+    h3a_status rc = packed_check(d, &plan, &rows_bytes, &bytes);
+    if (rc != H3A_OK) return rc;
+    if (d->total_q == 0 || d->max_q == 0) return H3A_OK;  // no query, nothing to write
+    if (!q || !o || (d->total_k > 0 && (!k || !v)) || !starts_q || !starts_k) return H3A_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return H3A_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(starts_q), static_cast<const void*>(starts_k),
+                          static_cast<const void*>(lengths_k), static_cast<const void*>(lse)})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return H3A_ERR_INVALID_ARG;
+    if (bytes > 0 && (!workspace || !aligned16(workspace) || ws_bytes < bytes)) return H3A_ERR_WORKSPACE;
+    PackedArgs a{};
+    a.q = q, a.k = k, a.v = v, a.o = o, a.lse = lse;
+    a.starts_q = starts_q, a.starts_k = starts_k, a.lengths_k = lengths_k;
+    a.qn = d->q_stride_n, a.qh = d->q_stride_h, a.kn = d->k_stride_n, a.kh = d->k_stride_h;
+    a.vn = d->v_stride_n, a.vh = d->v_stride_h, a.on = d->o_stride_n, a.oh = d->o_stride_h;
+    a.total_q = d->total_q, a.total_k = d->total_k, a.max_q = d->max_q;
+    a.seqs = d->seqs, a.heads = d->heads, a.kv_heads = d->kv_heads, a.group = d->heads / d->kv_heads;
+    a.causal = d->causal != 0;
+    const double scale = d->scale == 0.0f ? 1.0 / std::sqrt(static_cast<double>(d->head_dim)) : d->scale;
+    a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    a.splits = plan.splits, a.chunk = plan.chunk;
+    if (plan.splits > 1) {
+        a.part_o = static_cast<float*>(workspace);
+        a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes);
+    }
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_packed_rows(a, d->head_dim, d->dtype == H3A_FP16, plan.row_blocks, st);
+    if (e == cudaSuccess && plan.splits > 1) e = launch_packed_combine(a, d->head_dim, d->dtype == H3A_FP16, st);
     return e == cudaSuccess ? H3A_OK : cuda_fail(e);
 }
 

@@ -1,0 +1,365 @@
+// Attention over packed sequences, few query rows at a time: single tokens
+// over caches (h3a_packed_attention; the tile kernel in packed_tiles.cu takes
+// calls with more rows).
+//
+// The queries that share a kv head are the rows of one matrix: row r of a
+// sequence is query r / group, head r % group of the kv head's group.  A CTA
+// takes 16 of them (the M of mma.m16n8k16) and one part of the sequence's keys;
+// its warps take units of 16 keys in turn, each with a cp.async pipeline of its
+// own through shared memory, so no barrier stands between load and use:
+//   S = Q K^T (Q in registers), online softmax in fp32 (log2 domain, running
+//   row maximum m and sum l), O = alpha O + P V with P rounded to the element
+//   type straight from S's registers.
+// At the end the warps' (m, l, O) are joined through shared memory, and, when
+// the keys were split over CTAs, written as a normalised fp32 row with its
+// log-sum-exp for packed_combine.cu.  HBM-bound: K and V are read once per 16
+// rows; one unit is 16 keys x (K + V) = 8 KB at head_dim 128.
+//
+// Keys no row of the CTA attends are read as zeros (cp.async with a source
+// size of 0), so what lies behind a sequence is never touched.  Where some rows
+// attend a key and others do not (causal, several queries), an infinity or NaN
+// in V would reach the others as 0 * NaN: such a unit's V fragments have their
+// non-finite values set to zero, and the epilogue adds those back to exactly
+// the rows that attend them.
+#include "half16.cuh"
+#include "prompt_internal.h"
+
+namespace h3a {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnit = 16;    // keys a warp takes at a time
+constexpr int kStages = 3;
+
+template <int D>
+struct Geo {
+    static constexpr int kPitch = D * 2 + 16;  // an odd multiple of 16 bytes: ldmatrix rows hit distinct banks
+    static constexpr int kTile = kUnit * kPitch;
+    static constexpr int kChunks = D / 8;      // 16-byte chunks of a key
+    static constexpr int kStageBytes = 2 * kTile;
+    static constexpr int kPipeBytes = kWarps * kStages * kStageBytes;
+    static constexpr int kJoinPitch = D + 4;
+    static constexpr int kJoinBytes = (kWarps * 16 * kJoinPitch + kWarps * 16 * 2) * 4;
+    static constexpr int kSmem = kPipeBytes > kJoinBytes ? kPipeBytes : kJoinBytes;
+    static_assert(D % 16 == 0 && (kUnit * kChunks) % 32 == 0, "head_dim");
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes global -> shared; zeros when `bytes` is 0 (nothing is read then)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <bool FP16>
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (FP16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedArgs a, int row_blocks) {
+    using G = Geo<D>;
+    using H = Half16<FP16>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int found_nonfinite;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // split slowest: the parts that short sequences do not have come last
+    uint32_t at = blockIdx.x;
+    const int rb = at % row_blocks;
+    at /= row_blocks;
+    const int kvh = at % a.kv_heads;
+    at /= a.kv_heads;
+    const int seq = at % a.seqs, split = at / a.seqs;
+    const PackedSeq s = packed_seq(a, seq);
+    const int64_t rows = min(static_cast<int64_t>(s.lq), a.max_q) * a.group;
+    const int64_t r0 = static_cast<int64_t>(rb) * 16;
+    if (r0 >= rows) return;
+    const int first_query = static_cast<int>(r0 / a.group);
+    const int last_query = static_cast<int>(min(r0 + 15, rows - 1) / a.group);
+    const int least = packed_limit(a, s, first_query), most = packed_limit(a, s, last_query);
+    // this part's keys; the last part takes what remains, the first is never left out
+    const int begin = split == 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(split) * a.chunk, static_cast<int64_t>(most)));
+    const int end = split + 1 == a.splits ? most : static_cast<int>(min((split + 1) * static_cast<int64_t>(a.chunk), static_cast<int64_t>(most)));
+    if (split > 0 && begin >= end) return;  // the combine does not read parts past a row's keys
+    if (threadIdx.x == 0) found_nonfinite = 0;
+    __syncthreads();
+
+    // Q: rows lane / 4 and lane / 4 + 8 of the A fragments
+    const int ra = lane >> 2;
+    int limit[2];
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int64_t r = r0 + ra + 8 * e;
+        const bool in = r < rows;
+        const int query = static_cast<int>(in ? r / a.group : 0), head = static_cast<int>(in ? r % a.group : 0);
+        limit[e] = in ? packed_limit(a, s, query) : 0;
+        const uint16_t* p = static_cast<const uint16_t*>(a.q) + (s.q0 + query) * a.qn + (static_cast<int64_t>(kvh) * a.group + head) * a.qh;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const int c = ks * 16 + 2 * (lane & 3);
+            qf[ks][e] = in ? *reinterpret_cast<const uint32_t*>(p + c) : 0u;
+            qf[ks][e + 2] = in ? *reinterpret_cast<const uint32_t*>(p + c + 8) : 0u;
+        }
+    }
+
+    const uint32_t pipe = smem_addr(smem) + warp * (kStages * G::kStageBytes);
+    const uint16_t* kbase = static_cast<const uint16_t*>(a.k) + s.k0 * a.kn + kvh * a.kh;
+    const uint16_t* vbase = static_cast<const uint16_t*>(a.v) + s.k0 * a.vn + kvh * a.vh;
+    auto load = [&](int key0, int stage) {
+        if (key0 < end) {
+            const uint32_t dk = pipe + stage * G::kStageBytes;
+#pragma unroll
+            for (int it = 0; it < kUnit * G::kChunks / 32; ++it) {
+                const int i = it * 32 + lane, row = i / G::kChunks, c = i % G::kChunks;
+                const int key = key0 + row;
+                const bool in = key < end;
+                const int64_t kk = in ? key : 0;
+                const uint32_t off = row * G::kPitch + c * 16;
+                cp_async16(dk + off, kbase + kk * a.kn + c * 8, in ? 16u : 0u);
+                cp_async16(dk + G::kTile + off, vbase + kk * a.vn + c * 8, in ? 16u : 0u);
+            }
+        }
+        cp_async_commit();  // an empty group keeps the count
+    };
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    bool nonfinite = false;
+    constexpr int kStride = kUnit * kWarps;
+    int next = begin + warp * kUnit;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i, next += kStride) load(next, i);
+    int stage = 0;
+    for (int key0 = begin + warp * kUnit; key0 < end; key0 += kStride, next += kStride) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        load(next, stage == 0 ? kStages - 1 : stage - 1);
+        const uint32_t kt = pipe + stage * G::kStageBytes, vt = kt + G::kTile;
+        // S = Q K^T: n-tiles of keys 0-7 and 8-15
+        float c[2][4] = {};
+        const int mi = lane >> 3, mr = lane & 7;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t b[4];
+            ldmatrix_x4(kt + ((mi >> 1) * 8 + mr) * G::kPitch + ks * 32 + (mi & 1) * 16, b);
+            mma_16x8x16<FP16>(c[0], qf[ks], b[0], b[1]);
+            mma_16x8x16<FP16>(c[1], qf[ks], b[2], b[3]);
+        }
+        const bool partly = key0 + kUnit > least;  // some row does not attend some key of the unit
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                c[t][e] *= a.scale_log2;
+                if (partly && key0 + t * 8 + 2 * (lane & 3) + (e & 1) >= min(limit[e >> 1], end)) c[t][e] = -INFINITY;
+                mx[e >> 1] = fmaxf(mx[e >> 1], c[t][e]);
+            }
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+            mx[e] = fmaxf(mx[e], m[e]);
+            const float ref = mx[e] == -INFINITY ? 0.f : mx[e];  // no key yet: every weight is exp2(-inf) = 0
+            alpha[e] = exp2_fast(m[e] - ref);
+            m[e] = mx[e];
+            l[e] *= alpha[e];
+            mx[e] = ref;
+        }
+        uint32_t p[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                c[t][e] = exp2_fast(c[t][e] - mx[e >> 1]);
+                l[e >> 1] += c[t][e];
+            }
+            p[2 * t] = H::pack(c[t][0], c[t][1]);
+            p[2 * t + 1] = H::pack(c[t][2], c[t][3]);
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                o[i][0] *= alpha[0], o[i][1] *= alpha[0];
+                o[i][2] *= alpha[1], o[i][3] *= alpha[1];
+            }
+        }
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) {
+            uint32_t b[4];
+            ldmatrix_x4_trans(vt + ((mi & 1) * 8 + mr) * G::kPitch + dt * 32 + (mi >> 1) * 16, b);
+            if (partly) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t bad = nonfinite_halves<FP16>(b[i]);
+                    nonfinite |= bad != 0;
+                    b[i] = finite_or_zero<FP16>(b[i], bad);
+                }
+            }
+            mma_16x8x16<FP16>(o[2 * dt], p, b[0], b[1]);
+            mma_16x8x16<FP16>(o[2 * dt + 1], p, b[2], b[3]);
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    }
+    if (nonfinite) found_nonfinite = 1;
+    __syncthreads();  // every warp is done with its pipeline: the join reuses it
+    float* jo = reinterpret_cast<float*>(smem);
+    float* jm = jo + kWarps * 16 * G::kJoinPitch;
+    float* jl = jm + kWarps * 16;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        float* d = jo + (warp * 16 + ra) * G::kJoinPitch + i * 8 + 2 * (lane & 3);
+        *reinterpret_cast<float2*>(d) = make_float2(o[i][0], o[i][1]);
+        *reinterpret_cast<float2*>(d + 8 * G::kJoinPitch) = make_float2(o[i][2], o[i][3]);
+    }
+    if ((lane & 3) == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            jm[warp * 16 + ra + 8 * e] = m[e];
+            jl[warp * 16 + ra + 8 * e] = l[e];
+        }
+    }
+    __syncthreads();
+    // eight threads a row, every eighth group of four channels each
+    const int row = threadIdx.x >> 3;
+    const int64_t r = r0 + row;
+    if (r >= rows) return;
+    const int query = static_cast<int>(r / a.group);
+    const int64_t n = s.q0 + query;
+    const int head = kvh * a.group + static_cast<int>(r % a.group);
+    float top = -INFINITY, w[kWarps], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, jm[i * 16 + row]);
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        w[i] = exp2_fast(jm[i * 16 + row] - ref);
+        sum += w[i] * jl[i * 16 + row];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    const float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
+    const int64_t qh = n * a.heads + head;
+    const int limit_row = min(packed_limit(a, s, query), end);
+    for (int c = (threadIdx.x & 7) * 4; c < D; c += 32) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(jo + (i * 16 + row) * G::kJoinPitch + c);
+            acc.x = fmaf(w[i], v.x, acc.x), acc.y = fmaf(w[i], v.y, acc.y);
+            acc.z = fmaf(w[i], v.z, acc.z), acc.w = fmaf(w[i], v.w, acc.w);
+        }
+        acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+        if (found_nonfinite) {
+            // the units whose V was cleared: from the first key some row does not attend
+            const int from = max(begin, begin + (least - begin) / kUnit * kUnit);
+            for (int key = from; key < limit_row; ++key) {
+                const uint2 raw = *reinterpret_cast<const uint2*>(vbase + static_cast<int64_t>(key) * a.vn + c);
+                float x[4];
+                H::unpack(raw.x, x[0], x[1]);
+                H::unpack(raw.y, x[2], x[3]);
+                acc.x += isfinite(x[0]) ? 0.f : x[0], acc.y += isfinite(x[1]) ? 0.f : x[1];
+                acc.z += isfinite(x[2]) ? 0.f : x[2], acc.w += isfinite(x[3]) ? 0.f : x[3];
+            }
+        }
+        if (a.splits > 1) {
+            *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(split) * a.total_q * a.heads + qh) * D + c) = acc;
+        } else {
+            uint16_t* dst = static_cast<uint16_t*>(a.o) + n * a.on + head * a.oh + c;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(H::pack(acc.x, acc.y), H::pack(acc.z, acc.w));
+        }
+    }
+    if ((threadIdx.x & 7) == 0) {
+        if (a.splits > 1)
+            a.part_lse[static_cast<int64_t>(split) * a.total_q * a.heads + qh] = lse2;
+        else if (a.lse)
+            a.lse[qh] = lse2 * 0.6931471805599453f;
+    }
+}
+
+template <int D, bool FP16>
+cudaError_t run(const PackedArgs& a, int row_blocks, cudaStream_t st) {
+    constexpr int smem = Geo<D>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(packed_rows_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(a.seqs) * a.kv_heads * row_blocks * a.splits;
+    packed_rows_kernel<D, FP16><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a, row_blocks);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+PackedPlan packed_plan(const h3a_packed_desc& d) {
+    PackedPlan p;
+    const int64_t group = d.heads / d.kv_heads;
+    const int64_t max_q = d.max_q < d.total_q ? d.max_q : d.total_q;
+    const int64_t blocks = (max_q * group + 15) / 16;
+    p.row_blocks = static_cast<int>(blocks < (int64_t(1) << 30) ? blocks : (int64_t(1) << 30));
+    // Keys of a part: small enough that the parts fill the GPU about twice over
+    // and long sequences do not outlast the rest, at least 128 (a part costs
+    // each of its rows a partial row), at most 1,024.
+    const int64_t max_k = d.max_k < d.total_k ? d.max_k : d.total_k;
+    const int64_t base = static_cast<int64_t>(d.seqs) * d.kv_heads * (blocks > 0 ? blocks : 1);
+    int64_t chunk = max_k * base / (4 * kSms) / 64 * 64;
+    chunk = chunk < 128 ? 128 : chunk > 1024 ? 1024 : chunk;
+    int64_t splits = (max_k + chunk - 1) / chunk;
+    if (splits > 256) {
+        splits = 256;
+        chunk = ((max_k + 255) / 256 + 63) / 64 * 64;
+    }
+    p.splits = static_cast<int>(splits < 1 ? 1 : splits);
+    p.chunk = static_cast<int>(chunk);
+    return p;
+}
+
+cudaError_t launch_packed_rows(const PackedArgs& a, int d, bool fp16, int row_blocks, cudaStream_t st) {
+    if (row_blocks == 0) return cudaSuccess;
+    switch (d) {
+        case 64: return fp16 ? run<64, true>(a, row_blocks, st) : run<64, false>(a, row_blocks, st);
+        case 96: return fp16 ? run<96, true>(a, row_blocks, st) : run<96, false>(a, row_blocks, st);
+        default: return fp16 ? run<128, true>(a, row_blocks, st) : run<128, false>(a, row_blocks, st);
+    }
+}
+
+}  // namespace h3a

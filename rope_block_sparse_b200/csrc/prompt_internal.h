@@ -1,0 +1,95 @@
+// Launchers of the prompt side's operators, shared between the C-ABI front end
+// (h3a_api.cu) and the kernel translation units.  Not part of the public
+// interface.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+#include "h3a.h"
+
+namespace h3a {
+
+constexpr int kSms = 148;  // B200
+
+// One-dimensional rotary positions (rope.cu).  A side with heads == 0 is absent.
+struct RopeSide {
+    const void* x;
+    void* y;
+    int64_t sn, sh, on, oh;  // element strides of input and output
+    int heads;
+};
+cudaError_t launch_rope(const RopeSide& q, const RopeSide& k, int head_dim, bool fp16, const int32_t* positions,
+                        int64_t tokens, const h3a_rope_plan& plan, bool inverse, cudaStream_t st);
+
+// Residual addition + RMS norm (rmsnorm.cu).
+struct RmsNormArgs {
+    const void* x;
+    const void* f;  // null: no residual
+    const float* gamma;
+    void* h;
+    void* y;
+    float* scales;
+    int64_t xs, fs, hs, ys;  // row strides, elements
+    int64_t rows;
+    int width;
+    float eps;
+};
+constexpr int kRmsNormMaxWidth = 16384;
+cudaError_t launch_residual_rmsnorm(const RmsNormArgs& a, bool fp16, h3a_scales scales, cudaStream_t st);
+
+// Attention over packed sequences (packed_rows.cu, packed_combine.cu).
+struct PackedArgs {
+    const void *q, *k, *v;
+    void* o;
+    float* lse;  // [total_q, heads] or null
+    const int32_t *starts_q, *starts_k, *lengths_k;
+    int64_t qn, qh, kn, kh, vn, vh, on, oh;  // element strides
+    int64_t total_q, total_k;
+    int64_t max_q;           // queries of a sequence past this are left alone
+    int seqs, heads, kv_heads, group;
+    int causal;
+    float scale_log2;  // logit scale * log2(e)
+    int splits;        // parts a sequence's keys may be cut into
+    int chunk;         // keys of each part (the last part takes what remains)
+    float* part_o;     // [splits, total_q, heads, d] when splits > 1: normalised rows
+    float* part_lse;   // [splits, total_q, heads], log2 units
+};
+// What a sequence's entry of the index arrays means, cut to the tensors.
+struct PackedSeq {
+    int64_t q0, k0;
+    int lq, lk;
+};
+__device__ __forceinline__ PackedSeq packed_seq(const PackedArgs& a, int s) {
+    PackedSeq r;
+    const int64_t tq = a.total_q, tk = a.total_k;
+    const int64_t q0 = min(max(static_cast<int64_t>(__ldg(a.starts_q + s)), int64_t(0)), tq);
+    const int64_t q1 = min(max(static_cast<int64_t>(__ldg(a.starts_q + s + 1)), q0), tq);
+    const int64_t k0 = min(max(static_cast<int64_t>(__ldg(a.starts_k + s)), int64_t(0)), tk);
+    const int64_t nk = a.lengths_k ? static_cast<int64_t>(__ldg(a.lengths_k + s))
+                                   : static_cast<int64_t>(__ldg(a.starts_k + s + 1)) - k0;
+    r.q0 = q0;
+    r.k0 = k0;
+    r.lq = static_cast<int>(q1 - q0);
+    r.lk = static_cast<int>(min(max(nk, int64_t(0)), tk - k0));
+    return r;
+}
+// Keys that query i of the sequence attends: the first `packed_limit` of it.
+__device__ __forceinline__ int packed_limit(const PackedArgs& a, const PackedSeq& s, int i) {
+    if (!a.causal) return s.lk;
+    const int64_t n = static_cast<int64_t>(i) + 1 + s.lk - s.lq;
+    return static_cast<int>(min(max(n, int64_t(0)), static_cast<int64_t>(s.lk)));
+}
+
+// How a call is carried out: see packed_plan (packed_rows.cu).
+struct PackedPlan {
+    int splits, chunk;
+    int row_blocks;  // blocks of 16 (query, head of the group) rows per sequence and kv head
+};
+PackedPlan packed_plan(const h3a_packed_desc& d);
+cudaError_t launch_packed_rows(const PackedArgs& a, int d, bool fp16, int row_blocks, cudaStream_t st);
+cudaError_t launch_packed_combine(const PackedArgs& a, int d, bool fp16, cudaStream_t st);
+
+}  // namespace h3a

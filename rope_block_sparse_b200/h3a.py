@@ -9,6 +9,7 @@ calls raise -- there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -27,7 +28,9 @@ EXPORTS = ("h3a_qk_norm_rope", "h3a_route_k", "h3a_route_workspace_size", "h3a_r
            "h3a_status_string", "h3a_last_cuda_error_string", "h3a_last_device_error",
            "h3a_selftest_wait_timeout", "h3a_selftest_mma", "h3a_selftest_exp2", "h3a_route_noalloc",
            "h3a_qk_norm_rope_pool", "h3a_route_pooled", "h3a_residual_adaln", "h3a_swiglu",
-           "h3a_residual_diff", "h3a_step_sparsity", "h3a_qk_fullnorm_rope")
+           "h3a_residual_diff", "h3a_step_sparsity", "h3a_qk_fullnorm_rope", "h3a_rope_plan_scaled",
+           "h3a_rope_plan_from", "h3a_rope", "h3a_residual_rmsnorm", "h3a_packed_attention_workspace_size",
+           "h3a_packed_attention")
 ROUTE_NOALLOC_MAX_BYTES = 64 << 20  # H3A_ROUTE_NOALLOC_MAX_BYTES
 RESIDUAL_DIFF_WORKSPACE_BYTES = 32768  # H3A_RESIDUAL_DIFF_WORKSPACE_BYTES
 
@@ -49,6 +52,27 @@ class QkvDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("stride_b", ctypes.c_int64), ("stride_n", ctypes.c_int64),
                 ("stride_h", ctypes.c_int64)]
+
+
+class HeadsDesc(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("stride_n", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("out_stride_n", ctypes.c_int64), ("out_stride_h", ctypes.c_int64)]
+
+
+class RopePlan(ctypes.Structure):
+    """Rotary frequencies of one model (h3a_rope_plan); made by rope_plan()."""
+    _fields_ = [("pairs", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128)]
+
+
+class PackedDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("seqs", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("total_q", ctypes.c_int64),
+                ("total_k", ctypes.c_int64), ("max_q", ctypes.c_int64), ("max_k", ctypes.c_int64),
+                ("q_stride_n", ctypes.c_int64), ("q_stride_h", ctypes.c_int64), ("k_stride_n", ctypes.c_int64),
+                ("k_stride_h", ctypes.c_int64), ("v_stride_n", ctypes.c_int64), ("v_stride_h", ctypes.c_int64),
+                ("o_stride_n", ctypes.c_int64), ("o_stride_h", ctypes.c_int64), ("causal", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -106,6 +130,19 @@ def load() -> ctypes.CDLL:
     lib.h3a_step_sparsity.restype = f64
     lib.h3a_qk_fullnorm_rope.argtypes = [P, P, ctypes.POINTER(QkvDesc), P, P, Grid, f64, f32, P, P, P]
     lib.h3a_qk_fullnorm_rope.restype = st
+    lib.h3a_rope_plan_scaled.argtypes = [i32, i32, f64, st, f64, i64, f64, f64, f64, ctypes.POINTER(RopePlan)]
+    lib.h3a_rope_plan_scaled.restype = st
+    lib.h3a_rope_plan_from.argtypes = [i32, i32, ctypes.POINTER(f64), f64, ctypes.POINTER(RopePlan)]
+    lib.h3a_rope_plan_from.restype = st
+    lib.h3a_rope.argtypes = [P, P, ctypes.POINTER(HeadsDesc), P, P, ctypes.POINTER(HeadsDesc), st, P, i64,
+                             ctypes.POINTER(RopePlan), i32, P]
+    lib.h3a_rope.restype = st
+    lib.h3a_residual_rmsnorm.argtypes = [P, i64, P, i64, P, i64, i32, st, f32, st, P, i64, P, i64, P, P]
+    lib.h3a_residual_rmsnorm.restype = st
+    lib.h3a_packed_attention_workspace_size.argtypes = [ctypes.POINTER(PackedDesc), ctypes.POINTER(ctypes.c_size_t)]
+    lib.h3a_packed_attention_workspace_size.restype = st
+    lib.h3a_packed_attention.argtypes = [P, P, P, ctypes.POINTER(PackedDesc), P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.h3a_packed_attention.restype = st
     _lib = lib
     return lib
 
@@ -376,6 +413,211 @@ def residual_diff(cur: torch.Tensor, prev: torch.Tensor, threshold: float = 0.04
                                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
                                                       _ptr(rel), _ptr(reuse), _stream_handle()))
     return rel, reuse
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # h3a_dtype
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}  # h3a_rope_scaling
+_SCALES = {None: 0, "row": 1, "group": 2}  # h3a_scales
+SCALE_GROUP = 128  # H3A_SCALE_GROUP
+
+
+def _launch(fn: str, device: torch.device, *args):
+    """Call an entry point on `device`'s current stream, whichever device is the current one."""
+    call, index = getattr(load(), fn), device.index
+    if index == torch.cuda.current_device():
+        _check(fn, call(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(index):
+            _check(fn, call(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _check_rows(name: str, t: torch.Tensor, dims: int, like: torch.Tensor | None = None) -> int:
+    """The h3a_dtype of a bf16 / fp16 CUDA tensor whose last dimension is contiguous."""
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (libh3a has no CPU path)")
+    if t.dim() != dims or t.stride(-1) != 1:
+        raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have the element type and device of the first tensor")
+    return dtype
+
+
+def _check_index(name: str, t: torch.Tensor, n: int, device: torch.device):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on {device}")
+
+
+def rope_plan(rotary_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+              factor: float = 1.0, original_length: int = 0, low_turns: float = 1.0, high_turns: float = 32.0,
+              amplitude: float = 1.0, frequencies=None) -> RopePlan:
+    """Rotary frequencies for rope(): theta^(-2j/rotary_dim), stretched for long contexts by `scaling`
+    ("none", "linear", "base", "parts": see h3a_rope_scaling), or the given `frequencies` (radians per
+    position, rotary_dim / 2 numbers).  interleaved: pairs (2j, 2j+1), else (j, j + rotary_dim/2).
+    Host only; plans of the same arguments are made once."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
+    return _rope_plan(int(rotary_dim), float(theta), bool(interleaved), scaling, float(factor), int(original_length),
+                      float(low_turns), float(high_turns), float(amplitude),
+                      None if frequencies is None else tuple(float(f) for f in frequencies))
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_plan(rotary_dim, theta, interleaved, scaling, factor, original_length, low_turns, high_turns, amplitude,
+               frequencies) -> RopePlan:
+    plan = RopePlan()
+    if frequencies is not None:
+        if len(frequencies) * 2 != rotary_dim:
+            raise ValueError("frequencies must hold rotary_dim / 2 numbers")
+        _check("h3a_rope_plan_from", load().h3a_rope_plan_from(
+            rotary_dim, interleaved, (ctypes.c_double * len(frequencies))(*frequencies), amplitude, ctypes.byref(plan)))
+    else:
+        _check("h3a_rope_plan_scaled", load().h3a_rope_plan_scaled(
+            rotary_dim, interleaved, theta, _ROPE_SCALINGS[scaling], factor, original_length, low_turns, high_turns,
+            amplitude, ctypes.byref(plan)))
+    return plan
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, plan: RopePlan, inverse: bool = False,
+         inplace: bool = False, out=None):
+    """One-dimensional rotary positions over bf16 or fp16 q [tokens, heads, head_dim] and k [tokens,
+    kv_heads, head_dim] (or None), any strides with head_dim contiguous (slices of a fused QKV buffer).
+    positions: int32 [tokens].  inverse rotates back.  Returns (q_out, k_out); inplace=True overwrites
+    q and k, out=(q_out, k_out) writes into given tensors."""
+    dtype = _check_rows("q", q, 3)
+    tokens, device = q.shape[0], q.device
+    _check_index("positions", positions, tokens, device)
+    xs = [q]
+    if k is not None:
+        _check_rows("k", k, 3, q)
+        if k.shape[0] != tokens or k.shape[2] != q.shape[2]:
+            raise ValueError("q and k must have the same tokens and head_dim")
+        xs.append(k)
+    if inplace:
+        ys = xs
+    elif out is not None:
+        ys = [y for y in out if y is not None]
+        if len(ys) != len(xs):
+            raise ValueError("out must hold a tensor for q, and for k where k is given")
+        for x, y in zip(xs, ys):
+            _check_rows("out", y, 3, q)
+            if y.shape != x.shape:
+                raise ValueError("out must have the shapes of q and k")
+    else:
+        ys = [x.new_empty(x.shape) for x in xs]
+    d = [HeadsDesc(x.shape[1], x.shape[2], x.stride(0), x.stride(1), y.stride(0), y.stride(1)) for x, y in zip(xs, ys)]
+    _launch("h3a_rope", device, q.data_ptr(), ys[0].data_ptr(), d[0], k.data_ptr() if k is not None else None,
+            ys[1].data_ptr() if k is not None else None, d[-1], dtype, positions.data_ptr(), tokens, plan, int(inverse))
+    return ys[0], (ys[1] if k is not None else None)
+
+
+def residual_rmsnorm(x: torch.Tensor, f: torch.Tensor | None, gamma: torch.Tensor, eps: float = 1e-6,
+                     scales: str | None = None, out=None):
+    """h = x + f, y = h / sqrt(mean(h^2) + eps) * gamma over the rows of bf16 or fp16 x and f [rows, C]
+    (row strides allowed; f None: h = x).  gamma: fp32 [C].  scales None: y in x's type; "row" or
+    "group" (128 channels): y in float8_e4m3fn with fp32 scales [rows] or [rows, ceil(C / 128)], so that
+    y * scale stands for the normalised row.  Returns (h or None, y, scales or None); out=(h, y, scales)
+    writes into given tensors (h may be x or f)."""
+    dtype = _check_rows("x", x, 2)
+    rows, width = x.shape
+    if scales not in _SCALES:
+        raise ValueError(f'scales must be None, "row" or "group", got {scales!r}')
+    if f is not None:
+        _check_rows("f", f, 2, x)
+        if f.shape != x.shape:
+            raise ValueError("f must match x")
+    if gamma.dtype != torch.float32 or gamma.shape != (width,) or not gamma.is_contiguous() or gamma.device != x.device:
+        raise ValueError("gamma must be a contiguous fp32 [C] tensor on x's device")
+    y_type = x.dtype if scales is None else torch.float8_e4m3fn
+    s_shape = None if scales is None else (rows,) if scales == "row" else (rows, -(-width // SCALE_GROUP))
+    if out is not None:
+        h, y, s = out
+        if f is not None:
+            _check_rows("h", h, 2, x)
+            if h.shape != x.shape:
+                raise ValueError("h must match x")
+        if y.dtype != y_type or y.shape != x.shape or y.stride(1) != 1 or y.device != x.device:
+            raise ValueError(f"y must be a {y_type} tensor of x's shape, rows contiguous")
+        if scales is not None and (s.dtype != torch.float32 or s.shape != s_shape or not s.is_contiguous()
+                                   or s.device != x.device):
+            raise ValueError(f"scales must be a contiguous fp32 {s_shape} tensor")
+    else:
+        h = x.new_empty(x.shape) if f is not None else None
+        y = x.new_empty(x.shape, dtype=y_type)
+        s = None if scales is None else gamma.new_empty(s_shape)
+    if f is None:
+        h = None
+    if scales is None:
+        s = None
+    _launch("h3a_residual_rmsnorm", x.device, x.data_ptr(), x.stride(0) if rows > 1 else width,
+            f.data_ptr() if f is not None else None, f.stride(0) if f is not None and rows > 1 else width,
+            gamma.data_ptr(), rows, width, dtype, float(eps), _SCALES[scales], h.data_ptr() if h is not None else None,
+            h.stride(0) if h is not None and rows > 1 else width, y.data_ptr(), y.stride(0) if rows > 1 else width,
+            s.data_ptr() if s is not None else None)
+    return h, y, s
+
+
+def _packed_desc(q, k, v, o, seqs, max_q, max_k, causal, scale) -> PackedDesc:
+    return PackedDesc(_DTYPES[q.dtype], seqs, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], int(max_q),
+                      int(max_k), q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                      o.stride(0), o.stride(1), int(causal), float(scale))
+
+
+def packed_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, seqs: int, max_q: int, max_k: int,
+                                    causal: bool = True) -> int:
+    """Bytes of workspace packed_attention() needs for these shapes (0: none)."""
+    n = ctypes.c_size_t(0)
+    d = _packed_desc(q, k, k, q, seqs, max_q, max_k, causal, 0.0)
+    _check("h3a_packed_attention_workspace_size",
+           load().h3a_packed_attention_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    return n.value
+
+
+def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts_q: torch.Tensor,
+                     starts_k: torch.Tensor, max_q: int, max_k: int, lengths_k: torch.Tensor | None = None,
+                     causal: bool = True, scale: float = 0.0, return_lse: bool = False,
+                     workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """Attention over packed sequences with grouped heads: q [total_q, heads, head_dim], k and v [total_k,
+    kv_heads, head_dim], bf16 or fp16, head_dim 64, 96 or 128 and contiguous.  Sequence s has the queries
+    starts_q[s]:starts_q[s+1] and the keys starts_k[s]:starts_k[s+1], or lengths_k[s] of them from
+    starts_k[s] on (a cache of fixed capacity).  causal: query i of lq attends keys j <= i + lk - lq, so whole
+    prompts, pieces of prompts and single tokens over a cache are the same call.  max_q and max_k: the
+    longest sequence's queries and keys (host numbers).  A query without keys gets zeros.  Returns o, or
+    (o, lse) with the natural log-sum-exps, fp32 [total_q, heads]; rows outside every sequence are left as
+    they were (in `out`) or undefined."""
+    dtype = _check_rows("q", q, 3)
+    device = q.device
+    _check_rows("k", k, 3, q)
+    _check_rows("v", v, 3, q)
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("k and v must have one shape, and q's head_dim")
+    seqs = starts_q.shape[0] - 1
+    _check_index("starts_q", starts_q, seqs + 1, device)
+    _check_index("starts_k", starts_k, seqs + 1, device)
+    if lengths_k is not None:
+        _check_index("lengths_k", lengths_k, seqs, device)
+    if out is None:
+        out = q.new_empty(q.shape)
+    else:
+        _check_rows("out", out, 3, q)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device) if return_lse else None
+    d = _packed_desc(q, k, v, out, seqs, max_q, max_k, causal, scale)
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        _check("h3a_packed_attention_workspace_size", load().h3a_packed_attention_workspace_size(d, n))
+        if n.value:
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    _launch("h3a_packed_attention", device, q.data_ptr(), k.data_ptr(), v.data_ptr(), d, starts_q.data_ptr(),
+            starts_k.data_ptr(), lengths_k.data_ptr() if lengths_k is not None else None, out.data_ptr(),
+            lse.data_ptr() if return_lse else None, workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return (out, lse) if return_lse else out
 
 
 def last_device_error() -> int:
