@@ -141,6 +141,26 @@ cudaError_t make_head_slice_tensor_map(CUtensorMap* map, const void* base, const
     return encode_qkv_map(map, base, s, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Tensor maps of the packed tile kernel (see launch_packed_tiles).  Without
+// keys, k and v may be null: q stands in, and no step reads it.
+static cudaError_t make_packed_tensor_maps(const h3a_packed_desc& d, const void* q, const void* k, const void* v,
+                                           CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv) {
+    const int group = d.heads / d.kv_heads;
+    // a dimension of size one is not stepped: any valid stride
+    auto step = [&](int64_t stride, int64_t size) { return size > 1 ? stride : static_cast<int64_t>(d.head_dim); };
+    const int64_t qh = step(d.q_stride_h, d.heads);
+    const Shape sq{static_cast<int>(d.total_q), d.kv_heads, group, d.head_dim, step(d.q_stride_n, d.total_q), qh * group, qh};
+    const cuuint32_t box[4] = {32, static_cast<cuuint32_t>(group), 1, static_cast<cuuint32_t>(packed_queries_per_tile(group))};
+    cudaError_t e = encode_qkv_map(tq, q, sq, box, CU_TENSOR_MAP_SWIZZLE_64B);
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+        const int64_t sn = step(i ? d.v_stride_n : d.k_stride_n, d.total_k), sh = step(i ? d.v_stride_h : d.k_stride_h, d.kv_heads);
+        const int rows = d.total_k > 0 ? static_cast<int>(d.total_k) : 1;
+        const Shape s{1, rows, d.total_k > 0 ? d.kv_heads : 1, d.head_dim, d.head_dim, sn, sh};
+        e = make_qkv_tensor_map(i ? tv : tk, d.total_k > 0 ? (i ? v : k) : q, s);
+    }
+    return e;
+}
+
 }  // namespace h3a
 
 using namespace h3a;
@@ -211,13 +231,19 @@ h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, size_t* rows
     if (d->heads / d->kv_heads > 128) return H3A_ERR_UNSUPPORTED;
     const int64_t lim = int64_t(1) << 31;
     if (d->total_q >= lim || d->total_k >= lim) return H3A_ERR_UNSUPPORTED;
+    // byte strides must stay within the tensor-map limit (2^40)
+    for (int64_t s : {d->q_stride_n, d->q_stride_h * (d->heads / d->kv_heads), d->k_stride_n, d->k_stride_h, d->v_stride_n,
+                      d->v_stride_h})
+        if (s >= (int64_t(1) << 39)) return H3A_ERR_UNSUPPORTED;
     if (!strides_ok(d->q_stride_n, d->q_stride_h, d->total_q, d->heads, d->head_dim) ||
         !strides_ok(d->k_stride_n, d->k_stride_h, d->total_k, d->kv_heads, d->head_dim) ||
         !strides_ok(d->v_stride_n, d->v_stride_h, d->total_k, d->kv_heads, d->head_dim) ||
         !strides_ok(d->o_stride_n, d->o_stride_h, d->total_q, d->heads, d->head_dim))
         return H3A_ERR_INVALID_ARG;
     *plan = packed_plan(*d);
-    const double grid = static_cast<double>(d->seqs) * d->kv_heads * plan->row_blocks * plan->splits;
+    const int group = d->heads / d->kv_heads;
+    const double columns = plan->tiles ? static_cast<double>(packed_tile_pairs(d->total_q, d->seqs, group)) : d->seqs;
+    const double grid = columns * d->kv_heads * plan->splits;
     const double rows = static_cast<double>(d->total_q) * d->heads;
     if (grid >= static_cast<double>(lim) || rows >= 4.0 * static_cast<double>(lim)) return H3A_ERR_UNSUPPORTED;
     *rows_bytes = *bytes = 0;
@@ -561,7 +587,18 @@ h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, con
         a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes);
     }
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_packed_rows(a, d->head_dim, d->dtype == H3A_FP16, plan.row_blocks, st);
+    cudaError_t e;
+    if (plan.tiles) {
+        int* status = nullptr;
+        rc = status_word(&status);
+        if (rc != H3A_OK) return rc;
+        CUtensorMap tq, tk, tv;
+        e = make_packed_tensor_maps(*d, q, k, v, &tq, &tk, &tv);
+        if (e == cudaSuccess)
+            e = launch_packed_tiles(tq, tk, tv, a, d->head_dim, d->dtype == H3A_FP16, status, kWaitLimitNs, st);
+    } else {
+        e = launch_packed_rows(a, d->head_dim, d->dtype == H3A_FP16, st);
+    }
     if (e == cudaSuccess && plan.splits > 1) e = launch_packed_combine(a, d->head_dim, d->dtype == H3A_FP16, st);
     return e == cudaSuccess ? H3A_OK : cuda_fail(e);
 }

@@ -1,0 +1,51 @@
+// How an h3a_packed_attention call is carried out: which kernel, and into how
+// many parts a sequence's keys are cut.  Host only; goes by the descriptor's
+// sizes, so the workspace size follows from the descriptor alone.
+#include <algorithm>
+
+#include "prompt_internal.h"
+
+namespace h3a {
+
+int packed_queries_per_tile(int group) { return 128 / group; }
+
+int64_t packed_tile_pairs(int64_t total_q, int seqs, int group) {
+    return total_q / (2 * packed_queries_per_tile(group)) + seqs;
+}
+
+PackedPlan packed_plan(const h3a_packed_desc& d) {
+    PackedPlan p{};
+    const int group = d.heads / d.kv_heads;
+    const int64_t max_q = std::min(d.max_q, d.total_q), max_k = std::min(d.max_k, d.total_k);
+    // Up to 16 rows (queries x heads of a group) fit one mma.m16n8k16 tile of
+    // the row kernel, which then reads the keys once; more go to the 128-row
+    // tiles of the tcgen05 kernel.
+    p.tiles = max_q * group > 16;
+    int64_t splits, chunk;
+    if (p.tiles) {
+        // a part for every multiprocessor without work, each of at least 512
+        // keys (a part costs each of its rows an fp32 row written and read)
+        const int64_t pairs = std::max<int64_t>(1, (d.total_q + 2 * packed_queries_per_tile(group) - 1) / (2 * packed_queries_per_tile(group)));
+        const int64_t work = pairs * d.kv_heads;
+        splits = std::min(kSms / std::max<int64_t>(work, 1), max_k / 512);
+        splits = std::max<int64_t>(1, std::min<int64_t>(splits, 64));
+        chunk = ((max_k + splits - 1) / splits + 127) / 128 * 128;
+    } else {
+        // Keys of a part: small enough that the parts fill the GPU about twice
+        // over and long sequences do not outlast the rest, at least 128 and at
+        // most 1,024.
+        const int64_t base = static_cast<int64_t>(d.seqs) * d.kv_heads;
+        chunk = max_k * base / (4 * kSms) / 64 * 64;
+        chunk = std::max<int64_t>(128, std::min<int64_t>(chunk, 1024));
+        splits = (max_k + chunk - 1) / chunk;
+        if (splits > 256) {
+            splits = 256;
+            chunk = ((max_k + 255) / 256 + 63) / 64 * 64;
+        }
+    }
+    p.splits = static_cast<int>(std::max<int64_t>(1, splits));
+    p.chunk = static_cast<int>(std::max<int64_t>(128, std::min<int64_t>(chunk, int64_t(1) << 30)));
+    return p;
+}
+
+}  // namespace h3a

@@ -4,7 +4,8 @@
 //
 // The queries that share a kv head are the rows of one matrix: row r of a
 // sequence is query r / group, head r % group of the kv head's group.  A CTA
-// takes 16 of them (the M of mma.m16n8k16) and one part of the sequence's keys;
+// takes all of them, at most 16 (the M of mma.m16n8k16), and one part of the
+// sequence's keys;
 // its warps take units of 16 keys in turn, each with a cp.async pipeline of its
 // own through shared memory, so no barrier stands between load and use:
 //   S = Q K^T (Q in registers), online softmax in fp32 (log2 domain, running
@@ -12,8 +13,8 @@
 //   type straight from S's registers.
 // At the end the warps' (m, l, O) are joined through shared memory, and, when
 // the keys were split over CTAs, written as a normalised fp32 row with its
-// log-sum-exp for packed_combine.cu.  HBM-bound: K and V are read once per 16
-// rows; one unit is 16 keys x (K + V) = 8 KB at head_dim 128.
+// log-sum-exp for packed_combine.cu.  HBM-bound: K and V are read once;
+// one unit is 16 keys x (K + V) = 8 KB at head_dim 128.
 //
 // Keys no row of the CTA attends are read as zeros (cp.async with a source
 // size of 0), so what lies behind a sequence is never touched.  Where some rows
@@ -89,7 +90,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 template <int D, bool FP16>
-__global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedArgs a, int row_blocks) {
+__global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedArgs a) {
     using G = Geo<D>;
     using H = Half16<FP16>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -97,18 +98,14 @@ __global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedAr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // split slowest: the parts that short sequences do not have come last
     uint32_t at = blockIdx.x;
-    const int rb = at % row_blocks;
-    at /= row_blocks;
     const int kvh = at % a.kv_heads;
     at /= a.kv_heads;
     const int seq = at % a.seqs, split = at / a.seqs;
     const PackedSeq s = packed_seq(a, seq);
-    const int64_t rows = min(static_cast<int64_t>(s.lq), a.max_q) * a.group;
-    const int64_t r0 = static_cast<int64_t>(rb) * 16;
-    if (r0 >= rows) return;
-    const int first_query = static_cast<int>(r0 / a.group);
-    const int last_query = static_cast<int>(min(r0 + 15, rows - 1) / a.group);
-    const int least = packed_limit(a, s, first_query), most = packed_limit(a, s, last_query);
+    const int queries = static_cast<int>(min(static_cast<int64_t>(s.lq), a.max_q));
+    const int rows = queries * a.group;  // at most 16
+    if (rows == 0) return;
+    const int least = packed_limit(a, s, 0), most = packed_limit(a, s, queries - 1);
     // this part's keys; the last part takes what remains, the first is never left out
     const int begin = split == 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(split) * a.chunk, static_cast<int64_t>(most)));
     const int end = split + 1 == a.splits ? most : static_cast<int>(min((split + 1) * static_cast<int64_t>(a.chunk), static_cast<int64_t>(most)));
@@ -122,9 +119,9 @@ __global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedAr
     uint32_t qf[D / 16][4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int64_t r = r0 + ra + 8 * e;
+        const int r = ra + 8 * e;
         const bool in = r < rows;
-        const int query = static_cast<int>(in ? r / a.group : 0), head = static_cast<int>(in ? r % a.group : 0);
+        const int query = in ? r / a.group : 0, head = in ? r % a.group : 0;
         limit[e] = in ? packed_limit(a, s, query) : 0;
         const uint16_t* p = static_cast<const uint16_t*>(a.q) + (s.q0 + query) * a.qn + (static_cast<int64_t>(kvh) * a.group + head) * a.qh;
 #pragma unroll
@@ -264,11 +261,10 @@ __global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedAr
     __syncthreads();
     // eight threads a row, every eighth group of four channels each
     const int row = threadIdx.x >> 3;
-    const int64_t r = r0 + row;
-    if (r >= rows) return;
-    const int query = static_cast<int>(r / a.group);
+    if (row >= rows) return;
+    const int query = row / a.group;
     const int64_t n = s.q0 + query;
-    const int head = kvh * a.group + static_cast<int>(r % a.group);
+    const int head = kvh * a.group + row % a.group;
     float top = -INFINITY, w[kWarps], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) top = fmaxf(top, jm[i * 16 + row]);
@@ -319,46 +315,22 @@ __global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedAr
 }
 
 template <int D, bool FP16>
-cudaError_t run(const PackedArgs& a, int row_blocks, cudaStream_t st) {
+cudaError_t run(const PackedArgs& a, cudaStream_t st) {
     constexpr int smem = Geo<D>::kSmem;
     cudaError_t e = cudaFuncSetAttribute(packed_rows_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(a.seqs) * a.kv_heads * row_blocks * a.splits;
-    packed_rows_kernel<D, FP16><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a, row_blocks);
+    const int64_t grid = static_cast<int64_t>(a.seqs) * a.kv_heads * a.splits;
+    packed_rows_kernel<D, FP16><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-PackedPlan packed_plan(const h3a_packed_desc& d) {
-    PackedPlan p;
-    const int64_t group = d.heads / d.kv_heads;
-    const int64_t max_q = d.max_q < d.total_q ? d.max_q : d.total_q;
-    const int64_t blocks = (max_q * group + 15) / 16;
-    p.row_blocks = static_cast<int>(blocks < (int64_t(1) << 30) ? blocks : (int64_t(1) << 30));
-    // Keys of a part: small enough that the parts fill the GPU about twice over
-    // and long sequences do not outlast the rest, at least 128 (a part costs
-    // each of its rows a partial row), at most 1,024.
-    const int64_t max_k = d.max_k < d.total_k ? d.max_k : d.total_k;
-    const int64_t base = static_cast<int64_t>(d.seqs) * d.kv_heads * (blocks > 0 ? blocks : 1);
-    int64_t chunk = max_k * base / (4 * kSms) / 64 * 64;
-    chunk = chunk < 128 ? 128 : chunk > 1024 ? 1024 : chunk;
-    int64_t splits = (max_k + chunk - 1) / chunk;
-    if (splits > 256) {
-        splits = 256;
-        chunk = ((max_k + 255) / 256 + 63) / 64 * 64;
-    }
-    p.splits = static_cast<int>(splits < 1 ? 1 : splits);
-    p.chunk = static_cast<int>(chunk);
-    return p;
-}
-
-cudaError_t launch_packed_rows(const PackedArgs& a, int d, bool fp16, int row_blocks, cudaStream_t st) {
-    if (row_blocks == 0) return cudaSuccess;
+cudaError_t launch_packed_rows(const PackedArgs& a, int d, bool fp16, cudaStream_t st) {
     switch (d) {
-        case 64: return fp16 ? run<64, true>(a, row_blocks, st) : run<64, false>(a, row_blocks, st);
-        case 96: return fp16 ? run<96, true>(a, row_blocks, st) : run<96, false>(a, row_blocks, st);
-        default: return fp16 ? run<128, true>(a, row_blocks, st) : run<128, false>(a, row_blocks, st);
+        case 64: return fp16 ? run<64, true>(a, st) : run<64, false>(a, st);
+        case 96: return fp16 ? run<96, true>(a, st) : run<96, false>(a, st);
+        default: return fp16 ? run<128, true>(a, st) : run<128, false>(a, st);
     }
 }
 

@@ -1,0 +1,704 @@
+// Attention over packed sequences on tcgen05 (h3a_packed_attention): whole
+// prompts and pieces of prompts, causal or not, with grouped heads.
+//
+// The queries that share a kv head are the rows of one matrix: row r of a
+// 128-row tile is query r / group, head r % group of the kv head's group, so a
+// tile holds T = 128 / group queries (rounded down) of all the group's heads
+// and K and V are loaded once for the whole group.  The tensor map of Q has the
+// group as a dimension, so one TMA box {32 channels, group, 1, T} is one
+// swizzled chunk of such a tile.  One CTA owns two consecutive tiles (2 T
+// queries) of one sequence and kv head and one part of its keys (all of them
+// unless there are too few tiles to fill the GPU).
+//
+// Which sequence a CTA belongs to is found without a schedule made beforehand:
+// sequence s may use the tile pairs from floor(starts_q[s] / 2T) + s on, which
+// is ascending in s and leaves each sequence at least the ceil(lq / 2T) that it
+// needs; at most `seqs` CTAs find nothing to do.  Later pairs of a sequence see
+// more keys when causal, so CTAs take them in descending order (the longest
+// first).
+//
+// The pipeline is that of attention.cu (which see for the measurements behind
+// it): warps 0-7 softmax (warpgroup t = tile t, thread = row), warp 8 the TMA
+// producer with K and V rings of 64-byte swizzled chunks, warp 9 QK^T (and, at
+// head_dim 128, PV), warp 10 PV.  S_t = Q_t K^T and O_t += P_t V accumulate in
+// TMEM in fp32; the softmax is online in fp32 against a row reference that
+// moves only when the maximum grew by 2^8; P is rounded to the element type for
+// the PV MMA, whose error (half a step relative a weight) is that of rounding
+// O once more.  What is different:
+//   - the first tile of a pair may need fewer steps than the second (n[0] <=
+//     n[1], causal); it then simply stops earlier;
+//   - every row has its own number of keys; a step whose 128 keys all rows of a
+//     warp attend skips the comparison;
+//   - warp 11 looks over V.  In a step where some row does not attend some key,
+//     a weight of zero times an infinity or NaN in V would be NaN; there it
+//     clears such values in shared memory before PV may read them (the
+//     barrier v_ready) and notes it, and the epilogue adds them back to the rows that
+//     do attend them.  Only the last one to three steps of a CTA are looked
+//     over; in the others the warp passes the barrier on.
+#include "fastmath.cuh"
+#include "h3a_internal.h"
+#include "half16.cuh"
+#include "prompt_internal.h"
+#include "sm100.cuh"
+
+namespace h3a {
+namespace {
+
+constexpr int kSoftmaxWarps = 8;  // 2 warpgroups: one per query tile
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kPvWarp = 10, kScanWarp = 11;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+// Register split (setmaxnreg): the softmax warpgroups hold a 128-value row each.
+constexpr uint32_t kRegsLaunch = (65536 / kThreads) / 8 * 8;
+constexpr uint32_t kRegsSoftmax = 200, kRegsOther = 80;
+static_assert(kSoftmaxWarps * 32 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
+constexpr int kChunkBytes = 128 * 64;  // 128 rows x 32 channels, 64-byte swizzle
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSwizzle64 = 4;
+__host__ __device__ constexpr uint32_t col_s(int t) { return t ? 128u : 0u; }
+
+template <int D>
+struct Geo {
+    static constexpr int kChunks = D / 32;
+    static constexpr int kTileBytes = kChunks * kChunkBytes;
+    static constexpr int kStages = D == 64 ? 5 : D == 96 ? 3 : 2;
+    static constexpr int kKSteps = D / 16;
+    __host__ __device__ static constexpr uint32_t col_o(int t) { return 256u + (t ? D : 0); }
+    // Up to D = 96 a P buffer of 64 columns stands behind O_1 and the tiles take
+    // it in turn; at D = 128 P_t is written over S_t.
+    static constexpr bool kSepP = D <= 96;
+    static constexpr uint32_t kColP = 256u + 2 * D;
+    static_assert(!kSepP || kColP + 64 <= kTmemCols, "P buffer inside the allocation");
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kStages = Geo<D>::kStages;
+    uint8_t q[2][Geo<D>::kTileBytes];
+    uint8_t k[kStages][Geo<D>::kTileBytes];
+    uint8_t v[kStages][Geo<D>::kTileBytes];
+    uint64_t q_full[2];
+    uint64_t k_full[kStages], k_empty[kStages];
+    uint64_t v_full[kStages], v_ready[kStages], v_empty[kStages];
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t s_read[2];   // separate P: S_t has been read into registers
+    uint64_t pv_done[2];  // separate P: PV_t(j) has completed (P buffer free)
+    uint64_t mma_drain, pv_drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int never;      // stays 0: abort flag for waits that must ignore an abort
+    int nonfinite;  // warp 11 cleared a value of V
+};
+
+struct TileArgs {
+    PackedArgs p;
+    int pairs;     // tile pairs a kv head may have over all sequences
+    int per_tile;  // T: queries of a tile
+    int* status;
+    uint64_t timeout_ns;
+};
+
+// What one CTA works on.
+struct Work {
+    PackedSeq s;
+    int kvh, split;
+    int t0;        // first query of tile 0, in the sequence
+    int queries;   // queries of the sequence that count
+    int begin;     // first key of the part
+    int end0, end1;  // one past the last key any row of tile 0, 1 attends in this part
+    int n0, n1;      // 128-key steps of tile 0, 1
+    int last;        // the tile with the most steps: 1 if it exists, else 0
+    int clean;       // steps before the first in which some row does not attend some key
+    // selects, not arrays: an index known only at run time would put them in local memory
+    __device__ __forceinline__ int end(int t) const { return t ? end1 : end0; }
+    __device__ __forceinline__ int n(int t) const { return t ? n1 : n0; }
+    __device__ __forceinline__ int steps() const { return last ? n1 : n0; }
+};
+
+__device__ __forceinline__ void raise_timeout(const TileArgs& a, volatile int* abort_flag) {
+    *abort_flag = 1;
+    atomicOr(a.status, kDevTimeout);
+}
+
+__device__ __forceinline__ uint64_t kmajor_base(const uint8_t* tile) {
+    return smem_desc(smem_u32(tile), 16, 512, kSwizzle64);
+}
+__host__ __device__ constexpr uint32_t kmajor_step(int s) {
+    return static_cast<uint32_t>(((s >> 1) * kChunkBytes + (s & 1) * 32) >> 4);
+}
+__device__ __forceinline__ uint64_t mnmajor_base(const uint8_t* tile) {
+    return smem_desc(smem_u32(tile), kChunkBytes, 512, kSwizzle64);
+}
+__host__ __device__ constexpr uint32_t mnmajor_step(int s) { return static_cast<uint32_t>((s * 16 * 64) >> 4); }
+
+// Instruction descriptor of kind::f16 with fp32 accumulation; both operands bf16 or both fp16.
+template <bool FP16>
+constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
+    return idesc_bf16_f32(M, N, a_mn, b_mn) & ~(FP16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+// Finds this CTA's work; false if there is none.
+__device__ __forceinline__ bool find_work(const TileArgs& a, Work& w) {
+    uint32_t at = blockIdx.x;
+    const int pair = a.pairs - 1 - static_cast<int>(at % a.pairs);
+    at /= a.pairs;
+    w.kvh = at % a.p.kv_heads;
+    w.split = at / a.p.kv_heads;
+    const int span = 2 * a.per_tile;
+    auto first_pair = [&](int s) {
+        const int64_t q0 = min(max(static_cast<int64_t>(__ldg(a.p.starts_q + s)), int64_t(0)), a.p.total_q);
+        return static_cast<int>(q0 / span) + s;
+    };
+    int lo = 0, hi = a.p.seqs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_pair(mid) <= pair) lo = mid; else hi = mid;
+    }
+    const int64_t t0 = static_cast<int64_t>(pair - first_pair(lo)) * span;
+    w.s = packed_seq(a.p, lo);
+    w.queries = static_cast<int>(min(static_cast<int64_t>(w.s.lq), a.p.max_q));
+    if (t0 < 0 || t0 >= w.queries) return false;
+    w.t0 = static_cast<int>(t0);
+    w.last = w.t0 + a.per_tile < w.queries ? 1 : 0;
+    w.begin = 0;
+    w.end1 = w.n1 = 0;
+    for (int t = 0; t <= w.last; ++t) {
+        const int last_query = min(w.t0 + (t + 1) * a.per_tile, w.queries) - 1;
+        const int64_t limit = packed_limit(a.p, w.s, last_query);
+        const int64_t begin = min(static_cast<int64_t>(w.split) * a.p.chunk, int64_t(0x7fffffff) & ~int64_t(127));
+        const int64_t end = w.split + 1 == a.p.splits ? limit : min(limit, begin + a.p.chunk);
+        w.begin = static_cast<int>(begin);
+        const int n = end > begin ? static_cast<int>((end - begin + 127) / 128) : 0;
+        (t ? w.end1 : w.end0) = static_cast<int>(end);
+        (t ? w.n1 : w.n0) = n;
+    }
+    const int least = packed_limit(a.p, w.s, w.t0);
+    w.clean = least > w.begin ? (least - w.begin) / 128 : 0;
+    // later parts without keys are not read; the first one also stands for a row without any
+    return w.split == 0 || w.steps() > 0;
+}
+
+template <int D>
+__device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CUtensorMap* tq, const CUtensorMap* tk,
+                         const CUtensorMap* tv, volatile int* abort_flag) {
+    const uint32_t q_bytes = Geo<D>::kChunks * 64u * static_cast<uint32_t>(a.per_tile * a.p.group);
+    const int q0 = static_cast<int>(w.s.q0) + w.t0, k0 = static_cast<int>(w.s.k0) + w.begin;
+    for (int t = 0; t <= w.last; ++t) {
+        mbar_arrive_expect_tx(&sm.q_full[t], q_bytes);
+        for (int c = 0; c < Geo<D>::kChunks; ++c)
+            tma_load_4d(sm.q[t] + c * kChunkBytes, tq, &sm.q_full[t], 32 * c, 0, w.kvh, q0 + t * a.per_tile);
+    }
+    const int n = w.steps();
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    int issued_k = 0, issued_v = 0;
+    for (int j = 0; j < n; ++j) {
+        if (!(ok = mbar_wait(&sm.k_empty[stage], phase ^ 1u, abort_flag, a.timeout_ns))) break;
+        mbar_arrive_expect_tx(&sm.k_full[stage], Geo<D>::kTileBytes);
+        for (int c = 0; c < Geo<D>::kChunks; ++c)
+            tma_load_4d(sm.k[stage] + c * kChunkBytes, tk, &sm.k_full[stage], 32 * c, w.kvh, k0 + j * 128, 0);
+        ++issued_k;
+        if (!(ok = mbar_wait(&sm.v_empty[stage], phase ^ 1u, abort_flag, a.timeout_ns))) break;
+        mbar_arrive_expect_tx(&sm.v_full[stage], Geo<D>::kTileBytes);
+        for (int c = 0; c < Geo<D>::kChunks; ++c)
+            tma_load_4d(sm.v[stage] + c * kChunkBytes, tv, &sm.v_full[stage], 32 * c, w.kvh, k0 + j * 128, 0);
+        ++issued_v;
+        if (++stage == Geo<D>::kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    if (!ok) raise_timeout(a, abort_flag);
+    // Drain: every load issued must have landed before the CTA may exit.
+    volatile int* never = &sm.never;
+    for (int t = 0; t <= w.last; ++t) mbar_wait(&sm.q_full[t], 0u, never, a.timeout_ns);
+    for (int i = max(0, issued_k - Geo<D>::kStages); i < issued_k; ++i)
+        mbar_wait(&sm.k_full[i % Geo<D>::kStages], (i / Geo<D>::kStages) & 1u, never, a.timeout_ns);
+    for (int i = max(0, issued_v - Geo<D>::kStages); i < issued_v; ++i)
+        mbar_wait(&sm.v_full[i % Geo<D>::kStages], (i / Geo<D>::kStages) & 1u, never, a.timeout_ns);
+}
+
+// Warp 11: passes each V tile on, cleared of infinities and NaN where some row
+// does not attend some key of the step.
+template <int D, bool FP16>
+__device__ void scan_values(Smem<D>& sm, const TileArgs& a, const Work& w, volatile int* abort_flag) {
+    const int lane = threadIdx.x & 31, n = w.steps();
+    uint32_t stage = 0, phase = 0;
+    for (int j = 0; j < n; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.v_full[stage], phase, abort_flag, a.timeout_ns))) {
+            if (lane == 0) raise_timeout(a, abort_flag);
+            return;
+        }
+        if (j >= w.clean) {
+            uint4* tile = reinterpret_cast<uint4*>(sm.v[stage]);
+            uint32_t any = 0;
+#pragma unroll 4
+            for (int i = lane; i < Geo<D>::kTileBytes / 16; i += 32) {
+                uint4 x = tile[i];
+                const uint32_t b0 = nonfinite_halves<FP16>(x.x), b1 = nonfinite_halves<FP16>(x.y);
+                const uint32_t b2 = nonfinite_halves<FP16>(x.z), b3 = nonfinite_halves<FP16>(x.w);
+                if (b0 | b1 | b2 | b3) {
+                    any = 1;
+                    x.x = finite_or_zero<FP16>(x.x, b0), x.y = finite_or_zero<FP16>(x.y, b1);
+                    x.z = finite_or_zero<FP16>(x.z, b2), x.w = finite_or_zero<FP16>(x.w, b3);
+                    tile[i] = x;
+                }
+            }
+            if (any) *reinterpret_cast<volatile int*>(&sm.nonfinite) = 1;
+            fence_proxy_async_shared();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_ready[stage]);
+        if (++stage == Geo<D>::kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+}
+
+struct MmaState {
+    uint64_t dq0, dq1, dk, dv;  // base descriptors: Q tiles, K stage 0, V stage 0
+};
+
+// S_t(j) = Q_t K(j)^T.  The first tile of a step waits for K, the last one releases it.
+template <int D, bool FP16>
+__device__ __forceinline__ bool issue_qk(Smem<D>& sm, const TileArgs& a, const Work& w, const MmaState& st,
+                                         uint32_t tmem, int t, int j, volatile int* abort_flag) {
+    const uint32_t stage = static_cast<uint32_t>(j) % Geo<D>::kStages, phase = (static_cast<uint32_t>(j) / Geo<D>::kStages) & 1u;
+    if (!mbar_wait(&sm.k_full[stage], phase, abort_flag, a.timeout_ns)) return false;
+    tc_fence_after_sync();
+    constexpr uint32_t id = idesc<FP16>(128, 128, 0, 0);
+    const uint64_t dq = t ? st.dq1 : st.dq0, dk = st.dk + stage * (Geo<D>::kTileBytes >> 4);
+    const uint32_t d = tmem + col_s(t);
+#pragma unroll
+    for (int s = 0; s < Geo<D>::kKSteps; ++s) mma_ss(d, dq + kmajor_step(s), dk + kmajor_step(s), id, s > 0 ? 1u : 0u);
+    tc_commit(&sm.s_full[t]);
+    if (t == w.last) tc_commit(&sm.k_empty[stage]);
+    return true;
+}
+
+// O_t += P_t(j) V(j).
+template <int D, bool FP16>
+__device__ __forceinline__ bool issue_pv(Smem<D>& sm, const TileArgs& a, const Work& w, const MmaState& st,
+                                         uint32_t tmem, int t, int j, volatile int* abort_flag) {
+    const uint32_t stage = static_cast<uint32_t>(j) % Geo<D>::kStages, phase = (static_cast<uint32_t>(j) / Geo<D>::kStages) & 1u;
+    if (!mbar_wait(&sm.v_ready[stage], phase, abort_flag, a.timeout_ns)) return false;
+    tc_fence_after_sync();
+    constexpr uint32_t id = idesc<FP16>(128, D, 0, 1);
+    const uint64_t dv = st.dv + stage * (Geo<D>::kTileBytes >> 4);
+    const uint32_t d = tmem + Geo<D>::col_o(t), pa = tmem + (Geo<D>::kSepP ? Geo<D>::kColP : col_s(t));
+    mma_ts(d, pa, dv, id, j > 0 ? 1u : 0u);
+#pragma unroll
+    for (int s = 1; s < 8; ++s) mma_ts(d, pa + 8 * s, dv + mnmajor_step(s), id, 1u);
+    if (t == w.last) tc_commit(&sm.v_empty[stage]);
+    return true;
+}
+
+// Separate P: QK^T and PV touch disjoint TMEM and have a thread each.
+template <int D, bool FP16>
+__device__ void qk_issuer(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_t tmem, volatile int* abort_flag) {
+    if (w.steps() == 0) return;
+    MmaState st;
+    st.dq0 = kmajor_base(sm.q[0]);
+    st.dq1 = kmajor_base(sm.q[1]);
+    st.dk = kmajor_base(sm.k[0]);
+    bool ok = true;
+    for (int j = 0; j < w.steps() && ok; ++j)
+        for (int t = 0; t <= w.last && ok; ++t) {
+            if (j >= w.n(t)) continue;
+            ok = j == 0 ? mbar_wait(&sm.q_full[t], 0u, abort_flag, a.timeout_ns)
+                        : mbar_wait(&sm.s_read[t], static_cast<uint32_t>((j - 1) & 1), abort_flag, a.timeout_ns);
+            if (!ok) break;
+            tc_fence_after_sync();
+            ok = issue_qk<D, FP16>(sm, a, w, st, tmem, t, j, abort_flag);
+        }
+    if (!ok) raise_timeout(a, abort_flag);
+    // Drain: every MMA this thread issued must have completed before TMEM is released.
+    tc_commit(&sm.mma_drain);
+    mbar_wait(&sm.mma_drain, 0u, &sm.never, a.timeout_ns);
+}
+
+template <int D, bool FP16>
+__device__ void pv_issuer(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_t tmem, volatile int* abort_flag) {
+    if (w.steps() == 0) return;
+    MmaState st;
+    st.dv = mnmajor_base(sm.v[0]);
+    bool ok = true;
+    for (int j = 0; j < w.steps() && ok; ++j)
+        for (int t = 0; t <= w.last && ok; ++t) {
+            if (j >= w.n(t)) continue;
+            ok = mbar_wait(&sm.p_full[t], static_cast<uint32_t>(j & 1), abort_flag, a.timeout_ns);
+            if (!ok) break;
+            tc_fence_after_sync();
+            ok = issue_pv<D, FP16>(sm, a, w, st, tmem, t, j, abort_flag);
+            if (!ok) break;
+            tc_commit(&sm.pv_done[t]);
+            if (j + 1 == w.n(t)) tc_commit(&sm.o_done[t]);
+        }
+    if (!ok) raise_timeout(a, abort_flag);
+    tc_commit(&sm.pv_drain);
+    mbar_wait(&sm.pv_drain, 0u, &sm.never, a.timeout_ns);
+}
+
+// P over S: one thread, PV_t(j) then QK_t(j+1) per tile (the QK overwrites the
+// columns the PV reads; MMAs of one thread complete in issue order).
+template <int D, bool FP16>
+__device__ void mma_issuer(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_t tmem, volatile int* abort_flag) {
+    if (w.steps() == 0) return;
+    MmaState st;
+    st.dq0 = kmajor_base(sm.q[0]);
+    st.dq1 = kmajor_base(sm.q[1]);
+    st.dk = kmajor_base(sm.k[0]);
+    st.dv = mnmajor_base(sm.v[0]);
+    bool ok = true;
+    for (int t = 0; t <= w.last && ok; ++t)
+        if (w.n(t) > 0)
+            ok = mbar_wait(&sm.q_full[t], 0u, abort_flag, a.timeout_ns) && issue_qk<D, FP16>(sm, a, w, st, tmem, t, 0, abort_flag);
+    for (int j = 0; j < w.steps() && ok; ++j)
+        for (int t = 0; t <= w.last && ok; ++t) {
+            if (j >= w.n(t)) continue;
+            ok = mbar_wait(&sm.p_full[t], static_cast<uint32_t>(j & 1), abort_flag, a.timeout_ns);
+            if (!ok) break;
+            tc_fence_after_sync();
+            ok = issue_pv<D, FP16>(sm, a, w, st, tmem, t, j, abort_flag);
+            if (!ok) break;
+            if (j + 1 < w.n(t))
+                ok = issue_qk<D, FP16>(sm, a, w, st, tmem, t, j + 1, abort_flag);
+            else
+                tc_commit(&sm.o_done[t]);
+        }
+    if (!ok) raise_timeout(a, abort_flag);
+    tc_commit(&sm.mma_drain);
+    mbar_wait(&sm.mma_drain, 0u, &sm.never, a.timeout_ns);
+}
+
+__device__ __forceinline__ uint32_t (&slice32(uint32_t* x))[32] { return *reinterpret_cast<uint32_t(*)[32]>(x); }
+__device__ __forceinline__ uint32_t (&slice16(uint32_t* x))[16] { return *reinterpret_cast<uint32_t(*)[16]>(x); }
+
+// O row *= alpha.  Out of line: it runs only when a row's maximum grew by more than 2^8.
+template <int D>
+__device__ __noinline__ void rescale_o(uint32_t tO, float alpha) {
+#pragma unroll 1
+    for (int cc = 0; cc < Geo<D>::kChunks; ++cc) {
+        uint32_t o[32];
+        tmem_ld_x32(tO + 32u * cc, o);
+        tmem_wait_ld_x32(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+        tmem_st_x32(tO + 32u * cc, o);
+    }
+}
+
+// Adds the infinities and NaN that 32 channels of V hold among keys [from, to)
+// to o: what warp 11 cleared, for a row that attends those keys.
+template <bool FP16>
+__device__ __noinline__ void add_nonfinite(float* o, const uint16_t* v, int64_t vn, int from, int to) {
+    for (int key = from; key < to; ++key) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(v + key * vn);
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t x = p[i];
+            if (nonfinite_halves<FP16>(x) == 0) continue;
+            float lo, hi;
+            Half16<FP16>::unpack(x, lo, hi);
+            o[2 * i] += isfinite(lo) ? 0.f : lo;
+            o[2 * i + 1] += isfinite(hi) ? 0.f : hi;
+        }
+    }
+}
+
+// Softmax of query tile t: thread r owns row r (TMEM lane r), all 128 keys of a step.
+template <int D, bool FP16>
+__device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_t tmem, int t, volatile int* abort_flag) {
+    using H = Half16<FP16>;
+    constexpr bool kSep = Geo<D>::kSepP;
+    const int lane = threadIdx.x & 31;
+    const int quarter = (threadIdx.x >> 5) & 3;  // TMEM lanes [32*quarter, 32*quarter + 32)
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_addr + col_s(t);
+    const uint32_t tO = tmem + lane_addr + Geo<D>::col_o(t);
+    const uint32_t tP = tmem + lane_addr + Geo<D>::kColP;
+    const int n = w.n(t);
+    const int query = w.t0 + t * a.per_tile + row / a.p.group;
+    const bool in = row < a.per_tile * a.p.group && query < w.queries;
+    // rows that are no query's see what the tile sees (and are not written), so
+    // that they do not cost their warp the comparisons
+    const int limit = in ? min(packed_limit(a.p, w.s, query), w.end(t)) : w.end(t);
+    int valid = max(limit - w.begin, 0);  // keys of the step and behind that the row attends
+    // Separate P: before this tile writes the shared P buffer at step j, the PV
+    // that last read it must have completed -- the other tile's of step j - 1
+    // (tile 0) or j (tile 1) as long as that tile runs, else this tile's own of
+    // step j - 1.  It was issued after PV_t(j-1), so O_t is stable too.  The
+    // wait names a phase at most one ahead of the barrier's last completed one.
+    auto wait_p_buffer = [&](int j) -> bool {
+        const bool other = t == 0 ? w.last == 1 : j < w.n0;
+        const int u = other ? 1 - t : t;
+        const int ph = other && t == 1 ? j : j - 1;
+        if (ph < 0) return true;
+        const bool r = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[u], static_cast<uint32_t>(ph & 1), abort_flag, a.timeout_ns));
+        if (r) tc_fence_after_sync();
+        return r;
+    };
+    const float c = a.p.scale_log2;
+    float m_used = -INFINITY;  // row reference of scaled logits (log2 units); -inf: no key yet
+    float l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j, valid -= 128) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[t], static_cast<uint32_t>(j & 1), abort_flag, a.timeout_ns))) {
+            ok = false;
+            break;
+        }
+        tc_fence_after_sync();
+        const bool partly = __any_sync(0xffffffffu, valid < 128);
+        uint32_t x[128];
+        float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) tmem_ld_x32(tS + 32u * q, slice32(x + 32 * q));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) tmem_wait_ld_x32(slice32(x + 32 * q));
+#pragma unroll
+        for (int q = 2; q < 4; ++q) tmem_ld_x32(tS + 32u * q, slice32(x + 32 * q));
+        if (partly) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (i >= valid) x[i] = __float_as_uint(-INFINITY);
+        }
+        // first half's max while the second half loads
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            pm[i & 3] = max3(pm[i & 3], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+#pragma unroll
+        for (int q = 2; q < 4; ++q) tmem_wait_ld_x32(slice32(x + 32 * q));
+        if constexpr (kSep) {
+            // S_t is in registers: release it for QK_t(j+1)
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_read[t]);
+        }
+        bool p_free = false;
+        if (partly) {
+#pragma unroll
+            for (int i = 64; i < 128; ++i)
+                if (i >= valid) x[i] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int i = 32; i < 64; ++i)
+            pm[i & 3] = max3(pm[i & 3], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+        const float mx = c * fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+        if (j == 0) {
+            m_used = mx;  // the first step fixes the reference
+        } else {
+            const bool need = mx - m_used > 8.0f;  // also a row's first key, from a reference of -inf
+            if (__any_sync(0xffffffffu, need)) {
+                // O_t must be stable: with P over S the commit behind s_full
+                // covers PV_t(j-1); with a separate P buffer, its wait does
+                if constexpr (kSep) {
+                    if (!wait_p_buffer(j)) {
+                        ok = false;
+                        break;
+                    }
+                    p_free = true;
+                }
+                float alpha = 1.0f;
+                if (need) {
+                    alpha = ex2_approx(m_used - mx);
+                    m_used = mx;
+                }
+                l *= alpha;
+                rescale_o<D>(tO, alpha);
+            }
+        }
+        const float ref = m_used == -INFINITY ? 0.f : m_used;  // no key yet: weights 2^-inf = 0
+        const uint64_t c2 = f2(c, c), nm2 = f2(-ref, -ref);
+        uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+            float a0, a1;
+            f2_split(f2_fma(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, nm2), a0, a1);
+            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+            acc[i & 1] = f2_add(acc[i & 1], f2(p0, p1));
+            x[i] = H::pack(p0, p1);
+            if constexpr (!kSep)
+                if ((i & 15) == 15) tmem_st_x16(tS + (i - 15), slice16(x + (i - 15)));
+        }
+        if constexpr (kSep) {
+            if (!p_free && !wait_p_buffer(j)) {
+                ok = false;
+                break;
+            }
+            tmem_st_x32(tP, slice32(x));
+            tmem_st_x32(tP + 32u, slice32(x + 32));
+        }
+        float s0, s1, s2, s3;
+        f2_split(acc[0], s0, s1);
+        f2_split(acc[1], s2, s3);
+        l += (s0 + s1) + (s2 + s3);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[t]);
+    }
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_done[t], 0u, abort_flag, a.timeout_ns));
+    if (!ok) {
+        raise_timeout(a, abort_flag);
+        return;
+    }
+    if (n == 0 && w.split > 0) return;
+    tc_fence_after_sync();
+    const bool cleared = *reinterpret_cast<volatile int*>(&sm.nonfinite) != 0;
+    const float inv_l = l == 0.f ? 0.f : 1.0f / l;
+    const float lse2 = l == 0.f ? -INFINITY : m_used + log2f(l);
+    const int head = w.kvh * a.p.group + row % a.p.group;
+    const int64_t tok = w.s.q0 + query, qh = tok * a.p.heads + head;
+    const bool split = a.p.splits > 1;
+    uint16_t* dst = static_cast<uint16_t*>(a.p.o) + tok * a.p.on + head * a.p.oh;
+    float* part = split ? a.p.part_o + (w.split * a.p.total_q * a.p.heads + qh) * D : nullptr;
+#pragma unroll 1
+    for (int cc = 0; cc < Geo<D>::kChunks; ++cc) {
+        uint32_t raw[32];
+        float o[32];
+        if (n > 0) {
+            tmem_ld_x32(tO + 32u * cc, raw);
+            tmem_wait_ld_x32(raw);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = n > 0 && l != 0.f ? __uint_as_float(raw[i]) * inv_l : 0.f;
+        if (!in) continue;
+        if (cleared) {
+            float tmp[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) tmp[i] = o[i];
+            add_nonfinite<FP16>(tmp, static_cast<const uint16_t*>(a.p.v) + w.s.k0 * a.p.vn + w.kvh * a.p.vh + 32 * cc, a.p.vn,
+                                w.begin + 128 * w.clean, limit);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = tmp[i];
+        }
+        if (split) {
+            float4* d4 = reinterpret_cast<float4*>(part + 32 * cc);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d4[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+            uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * cc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                d4[i] = make_uint4(H::pack(o[8 * i], o[8 * i + 1]), H::pack(o[8 * i + 2], o[8 * i + 3]),
+                                   H::pack(o[8 * i + 4], o[8 * i + 5]), H::pack(o[8 * i + 6], o[8 * i + 7]));
+        }
+    }
+    if (in) {
+        if (split)
+            a.p.part_lse[w.split * a.p.total_q * a.p.heads + qh] = lse2;
+        else if (a.p.lse)
+            a.p.lse[qh] = lse2 * 0.6931471805599453f;
+    }
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_tiles_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ TileArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = smem_u32(smem_raw);
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw + (((base + 1023u) & ~1023u) - base));
+    Work w;
+    if (!find_work(a, w)) return;
+
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sm.q_full[t], 1);
+            mbar_init(&sm.s_full[t], 1);
+            mbar_init(&sm.p_full[t], 4);  // one arrival per softmax warp of the tile
+            mbar_init(&sm.o_done[t], 1);
+            mbar_init(&sm.s_read[t], 4);
+            mbar_init(&sm.pv_done[t], 1);
+        }
+        for (int s = 0; s < Geo<D>::kStages; ++s) {
+            mbar_init(&sm.k_full[s], 1);
+            mbar_init(&sm.k_empty[s], 1);
+            mbar_init(&sm.v_full[s], 1);
+            mbar_init(&sm.v_ready[s], 1);
+            mbar_init(&sm.v_empty[s], 1);
+        }
+        mbar_init(&sm.mma_drain, 1);
+        mbar_init(&sm.pv_drain, 1);
+        sm.abort_flag = 0;
+        sm.never = 0;
+        sm.nonfinite = 0;
+        fence_barrier_init();
+    }
+    if (warp == kProducerWarp && (threadIdx.x & 31) == 0) {
+        prefetch_tensor_map(&tq);
+        prefetch_tensor_map(&tk);
+        prefetch_tensor_map(&tv);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = sm.tmem_base;
+    volatile int* abort_flag = &sm.abort_flag;
+
+    if (warp < kSoftmaxWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int t = warp >> 2;
+        if (t <= w.last) softmax_group<D, FP16>(sm, a, w, tmem, t, abort_flag);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        const bool one = (threadIdx.x & 31) == 0;
+        if (warp == kProducerWarp) {
+            if (one) producer<D>(sm, a, w, &tq, &tk, &tv, abort_flag);
+        } else if (warp == kMmaWarp) {
+            if (one) {
+                if constexpr (Geo<D>::kSepP)
+                    qk_issuer<D, FP16>(sm, a, w, tmem, abort_flag);
+                else
+                    mma_issuer<D, FP16>(sm, a, w, tmem, abort_flag);
+            }
+        } else if (warp == kPvWarp) {
+            if constexpr (Geo<D>::kSepP)
+                if (one) pv_issuer<D, FP16>(sm, a, w, tmem, abort_flag);
+        } else {
+            scan_values<D, FP16>(sm, a, w, abort_flag);
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, bool FP16>
+cudaError_t run(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TileArgs& a, cudaStream_t st) {
+    constexpr size_t smem = sizeof(Smem<D>) + 1024;  // + alignment slack
+    static_assert(smem <= 232448, "shared memory per CTA");
+    cudaError_t e = cudaFuncSetAttribute(packed_tiles_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(a.pairs) * a.p.kv_heads * a.p.splits;
+    packed_tiles_kernel<D, FP16><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(tq, tk, tv, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_packed_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& p,
+                                int d, bool fp16, int* status, uint64_t timeout_ns, cudaStream_t st) {
+    TileArgs a;
+    a.p = p;
+    a.pairs = static_cast<int>(packed_tile_pairs(p.total_q, p.seqs, p.group));
+    a.per_tile = packed_queries_per_tile(p.group);
+    a.status = status;
+    a.timeout_ns = timeout_ns;
+    switch (d) {
+        case 64: return fp16 ? run<64, true>(tq, tk, tv, a, st) : run<64, false>(tq, tk, tv, a, st);
+        case 96: return fp16 ? run<96, true>(tq, tk, tv, a, st) : run<96, false>(tq, tk, tv, a, st);
+        default: return fp16 ? run<128, true>(tq, tk, tv, a, st) : run<128, false>(tq, tk, tv, a, st);
+    }
+}
+
+}  // namespace h3a

@@ -40,7 +40,7 @@ struct RmsNormArgs {
 constexpr int kRmsNormMaxWidth = 16384;
 cudaError_t launch_residual_rmsnorm(const RmsNormArgs& a, bool fp16, h3a_scales scales, cudaStream_t st);
 
-// Attention over packed sequences (packed_rows.cu, packed_combine.cu).
+// Attention over packed sequences (packed_tiles.cu, packed_rows.cu, packed_combine.cu).
 struct PackedArgs {
     const void *q, *k, *v;
     void* o;
@@ -83,13 +83,23 @@ __device__ __forceinline__ int packed_limit(const PackedArgs& a, const PackedSeq
     return static_cast<int>(min(max(n, int64_t(0)), static_cast<int64_t>(s.lk)));
 }
 
-// How a call is carried out: see packed_plan (packed_rows.cu).
+// How a call is carried out (packed_plan.cu).
 struct PackedPlan {
+    bool tiles;      // 128-row tiles on tcgen05 (packed_tiles.cu), else 16 rows (packed_rows.cu)
     int splits, chunk;
-    int row_blocks;  // blocks of 16 (query, head of the group) rows per sequence and kv head
 };
 PackedPlan packed_plan(const h3a_packed_desc& d);
-cudaError_t launch_packed_rows(const PackedArgs& a, int d, bool fp16, int row_blocks, cudaStream_t st);
+// Queries in a 128-row tile, and the tile pairs that hold every sequence's.
+int packed_queries_per_tile(int group);
+int64_t packed_tile_pairs(int64_t total_q, int seqs, int group);
+
+// At most 16 rows (queries x group) of each sequence and kv head.
+cudaError_t launch_packed_rows(const PackedArgs& a, int d, bool fp16, cudaStream_t st);
+// Tensor maps: q as {d, group, kv_heads, total_q} with a {32, group, 1,
+// packed_queries_per_tile} box, k and v as {d, kv_heads, total_k} with {32, 1,
+// 128} boxes, 64-byte swizzle.
+cudaError_t launch_packed_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& p,
+                                int d, bool fp16, int* status, uint64_t timeout_ns, cudaStream_t st);
 cudaError_t launch_packed_combine(const PackedArgs& a, int d, bool fp16, cudaStream_t st);
 
 }  // namespace h3a
