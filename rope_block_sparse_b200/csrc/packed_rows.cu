@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedAr
 template <int D, bool FP16>
 cudaError_t run(const PackedArgs& a, cudaStream_t st) {
     constexpr int smem = Geo<D>::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(packed_rows_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(packed_rows_kernel<D, FP16>), smem, done);
     if (e != cudaSuccess) return e;
     const int64_t grid = static_cast<int64_t>(a.seqs) * a.kv_heads * a.splits;
     packed_rows_kernel<D, FP16><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);

@@ -676,8 +676,8 @@ template <int D, bool FP16>
 cudaError_t run(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TileArgs& a, cudaStream_t st) {
     constexpr size_t smem = sizeof(Smem<D>) + 1024;  // + alignment slack
     static_assert(smem <= 232448, "shared memory per CTA");
-    cudaError_t e = cudaFuncSetAttribute(packed_tiles_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(packed_tiles_kernel<D, FP16>), static_cast<int>(smem), done);
     if (e != cudaSuccess) return e;
     const int64_t grid = static_cast<int64_t>(a.pairs) * a.p.kv_heads * a.p.splits;
     packed_tiles_kernel<D, FP16><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(tq, tk, tv, a);

@@ -5,6 +5,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -13,6 +14,10 @@
 namespace h3a {
 
 constexpr int kSms = 148;  // B200
+
+// Lets `kernel` use `bytes` of dynamic shared memory, once per device and kernel
+// (`done`: a bit for each device, of its own for each kernel).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // One-dimensional rotary positions (rope.cu).  A side with heads == 0 is absent.
 struct RopeSide {

@@ -38,7 +38,9 @@ def check(x, y, positions, freq, interleaved, amplitude=1.0, inverse=False, labe
 
 # tokens, heads, kv heads, head_dim, rotated channels
 SHAPES = [(1, 1, 1, 64, 64), (16, 32, 8, 128, 128), (77, 28, 4, 96, 48), (1025, 5, 1, 128, 50), (3, 2, 2, 8, 2),
-          (333, 7, 7, 96, 12), (5, 3, 1, 512, 256), (2500, 8, 2, 128, 16), (9, 1, 1, 136, 136), (7, 130, 3, 64, 64)]
+          (333, 7, 7, 96, 12), (5, 3, 1, 512, 256), (2500, 8, 2, 128, 16), (9, 1, 1, 136, 136), (7, 130, 3, 64, 64),
+          (50, 9, 3, 128, 24), (4000, 4, 1, 128, 50), (3000, 5, 2, 96, 24), (5000, 1, 1, 96, 10), (2600, 3, 1, 128, 128), (40000, 1, 1, 8, 6),
+          (3001, 2, 1, 512, 254)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
