@@ -434,17 +434,14 @@ def _launch(fn: str, call, index: int, *args):
 
 # A single-token step's kernels take a few microseconds, so what follows keeps the host's part short:
 # what depends on shapes, strides and types alone (checks, descriptors) is worked out once for each
-# combination of them (_layout) and looked up after that.  Nothing of a tensor's contents or address is kept.
+# combination of them and looked up after that (fresh outputs follow from the inputs).  Nothing of a tensor's contents or address is kept.
 _layouts: dict = {}
 
 
-def _layout(key, make):
-    got = _layouts.get(key)
-    if got is None:
-        got = make()
-        if len(_layouts) >= 4096:
-            _layouts.clear()
-        _layouts[key] = got
+def _layout(key, got):
+    if len(_layouts) >= 4096:
+        _layouts.clear()
+    _layouts[key] = got
     return got
 
 
@@ -513,13 +510,14 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, plan:
     positions: int32 [tokens].  inverse rotates back.  Returns (q_out, k_out); inplace=True overwrites
     q and k, out=(q_out, k_out) writes into given tensors."""
     if inplace:
-        q_out, k_out = q, k
+        q_out, k_out, key = q, k, ("rope in place", _sig(q), _sig(k), _sig(positions))
     elif out is not None:
         q_out, k_out = out
+        key = ("rope out", _sig(q), _sig(k), _sig(q_out), _sig(k_out), _sig(positions))
     else:
         q_out, k_out = _empty(q), (None if k is None else _empty(k))
-    lay = _layout(("rope", _sig(q), _sig(k), _sig(q_out), _sig(k_out), _sig(positions)),
-                  lambda: _rope_layout(q, k, q_out, k_out, positions))
+        key = ("rope", _sig(q), _sig(k), _sig(positions))
+    lay = _layouts.get(key) or _layout(key, _rope_layout(q, k, q_out, k_out, positions))
     call, index, dtype, tokens, dq, dk = lay
     if k is None:
         _launch("h3a_rope", call, index, q.data_ptr(), q_out.data_ptr(), dq, None, None, None, dtype,
@@ -563,6 +561,7 @@ def residual_rmsnorm(x: torch.Tensor, f: torch.Tensor | None, gamma: torch.Tenso
             h = None
         if scales is None:
             s = None
+        key = ("rmsnorm out", scales, _sig(x), _sig(f), _sig(gamma), _sig(h), _sig(y), _sig(s))
     else:
         h = None if f is None else _empty(x)
         if scales is None:
@@ -570,9 +569,9 @@ def residual_rmsnorm(x: torch.Tensor, f: torch.Tensor | None, gamma: torch.Tenso
         else:
             y = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
             rows, width = x.shape
-            s = gamma.new_empty((rows,) if scales == "row" else (rows, -(-width // SCALE_GROUP)))
-    lay = _layout(("rmsnorm", scales, _sig(x), _sig(f), _sig(gamma), _sig(h), _sig(y), _sig(s)),
-                  lambda: _rmsnorm_layout(x, f, gamma, scales, h, y, s))
+            s = gamma.new_empty(rows if scales == "row" else (rows, -(-width // SCALE_GROUP)))
+        key = ("rmsnorm", scales, _sig(x), _sig(f), _sig(gamma))
+    lay = _layouts.get(key) or _layout(key, _rmsnorm_layout(x, f, gamma, scales, h, y, s))
     call, index, xs, fs, rows, width, dtype, code, hs, ys = lay
     _launch("h3a_residual_rmsnorm", call, index, x.data_ptr(), xs, None if f is None else f.data_ptr(), fs,
             gamma.data_ptr(), rows, width, dtype, eps, code, None if h is None else h.data_ptr(), hs, y.data_ptr(), ys,
@@ -633,8 +632,10 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts_q
     they were (in `out`) or undefined."""
     if out is None:
         out = _empty(q)
-    lay = _layout(("packed", _sig(q), _sig(k), _sig(v), _sig(out), _sig(starts_q), _sig(starts_k), _sig(lengths_k)),
-                  lambda: _packed_layout(q, k, v, out, starts_q, starts_k, lengths_k))
+        key = ("packed", _sig(q), _sig(k), _sig(v), _sig(starts_q), _sig(starts_k), _sig(lengths_k))
+    else:
+        key = ("packed out", _sig(q), _sig(k), _sig(v), _sig(starts_q), _sig(starts_k), _sig(lengths_k), _sig(out))
+    lay = _layouts.get(key) or _layout(key, _packed_layout(q, k, v, out, starts_q, starts_k, lengths_k))
     call, size_of, index, head, strides = lay
     d = PackedDesc(*head, max_q, max_k, *strides, causal, scale)
     if workspace is None:

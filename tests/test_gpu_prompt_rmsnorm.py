@@ -45,7 +45,8 @@ def check(x, f, gamma, scales, h, y, s, label=""):
     ref.within(y.double(), target, target.abs() * (2.0 ** -4 + 4 * rel) + 2.0 ** -10, label + " e4m3")
 
 
-SHAPES = [(1, 8), (5, 128), (3, 136), (8, 5376), (1023, 2000), (33, 1024), (7, 1032), (300, 4096), (4, 14336), (2, 16384), (2000, 96), (700, 5376)]
+SHAPES = [(1, 8), (5, 128), (3, 136), (8, 5376), (1023, 2000), (33, 1024), (7, 1032), (300, 4096), (4, 14336), (2, 16384), (2000, 96), (700, 5376),
+          (9000, 64), (40000, 120), (9001, 256), (3000, 392), (5000, 768), (2500, 8192)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
