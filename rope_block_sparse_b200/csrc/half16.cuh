@@ -24,6 +24,12 @@ struct Half16<false> {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
         return r;
     }
+    // acc + 0 * w by halves: NaN from an infinity or NaN on
+    __device__ static __forceinline__ uint32_t add_zero_times(uint32_t w, uint32_t acc) {
+        uint32_t r;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(acc));
+        return r;
+    }
     // Exponent bits of both halves, and what is added to find one that is all ones.
     static constexpr uint32_t kExponents = 0x7F807F80u, kStep = 0x00800080u;
 };
@@ -39,6 +45,11 @@ struct Half16<true> {
     __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    __device__ static __forceinline__ uint32_t add_zero_times(uint32_t w, uint32_t acc) {
+        uint32_t r;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(acc));
         return r;
     }
     static constexpr uint32_t kExponents = 0x7C007C00u, kStep = 0x04000400u;

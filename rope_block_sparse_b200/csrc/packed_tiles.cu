@@ -136,8 +136,10 @@ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
     return idesc_bf16_f32(M, N, a_mn, b_mn) & ~(FP16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// Finds this CTA's work; false if there is none.
+// Finds this CTA's work; false if there is none.  The whole warp takes part (the
+// search tries 32 sequences at a time: each try is a trip to memory).
 __device__ __forceinline__ bool find_work(const TileArgs& a, Work& w) {
+    const int lane = threadIdx.x & 31;
     uint32_t at = blockIdx.x;
     const int pair = a.pairs - 1 - static_cast<int>(at % a.pairs);
     at /= a.pairs;
@@ -148,10 +150,12 @@ __device__ __forceinline__ bool find_work(const TileArgs& a, Work& w) {
         const int64_t q0 = min(max(static_cast<int64_t>(__ldg(a.p.starts_q + s)), int64_t(0)), a.p.total_q);
         return static_cast<int>(q0 / span) + s;
     };
-    int lo = 0, hi = a.p.seqs;
+    int lo = 0, hi = a.p.seqs;  // the last sequence in [lo, hi) whose pairs start at or before this one
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_pair(mid) <= pair) lo = mid; else hi = mid;
+        const int step = (hi - lo + 31) / 32, probe = lo + (lane + 1) * step;
+        const uint32_t yes = __ballot_sync(0xffffffffu, probe < hi && first_pair(probe) <= pair);
+        lo += __popc(yes) * step;
+        hi = min(hi, lo + step);
     }
     const int64_t t0 = static_cast<int64_t>(pair - first_pair(lo)) * span;
     w.s = packed_seq(a.p, lo);
@@ -182,11 +186,13 @@ __device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CU
                          const CUtensorMap* tv, volatile int* abort_flag) {
     const uint32_t q_bytes = Geo<D>::kChunks * 64u * static_cast<uint32_t>(a.per_tile * a.p.group);
     const int q0 = static_cast<int>(w.s.q0) + w.t0, k0 = static_cast<int>(w.s.k0) + w.begin;
-    for (int t = 0; t <= w.last; ++t) {
+    auto load_q = [&](int t) {
         mbar_arrive_expect_tx(&sm.q_full[t], q_bytes);
         for (int c = 0; c < Geo<D>::kChunks; ++c)
             tma_load_4d(sm.q[t] + c * kChunkBytes, tq, &sm.q_full[t], 32 * c, 0, w.kvh, q0 + t * a.per_tile);
-    }
+    };
+    // a tile without steps needs no Q (its rows' zeros go out through that memory)
+    if (w.n0 > 0) load_q(0);
     const int n = w.steps();
     uint32_t stage = 0, phase = 0;
     bool ok = true;
@@ -197,6 +203,7 @@ __device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CU
         for (int c = 0; c < Geo<D>::kChunks; ++c)
             tma_load_4d(sm.k[stage] + c * kChunkBytes, tk, &sm.k_full[stage], 32 * c, w.kvh, k0 + j * 128, 0);
         ++issued_k;
+        if (j == 0 && w.n1 > 0) load_q(1);  // behind the K that the first tile waits for
         if (!(ok = mbar_wait(&sm.v_empty[stage], phase ^ 1u, abort_flag, a.timeout_ns))) break;
         mbar_arrive_expect_tx(&sm.v_full[stage], Geo<D>::kTileBytes);
         for (int c = 0; c < Geo<D>::kChunks; ++c)
@@ -210,7 +217,8 @@ __device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CU
     if (!ok) raise_timeout(a, abort_flag);
     // Drain: every load issued must have landed before the CTA may exit.
     volatile int* never = &sm.never;
-    for (int t = 0; t <= w.last; ++t) mbar_wait(&sm.q_full[t], 0u, never, a.timeout_ns);
+    if (w.n0 > 0) mbar_wait(&sm.q_full[0], 0u, never, a.timeout_ns);
+    if (issued_k > 0 && w.n1 > 0) mbar_wait(&sm.q_full[1], 0u, never, a.timeout_ns);
     for (int i = max(0, issued_k - Geo<D>::kStages); i < issued_k; ++i)
         mbar_wait(&sm.k_full[i % Geo<D>::kStages], (i / Geo<D>::kStages) & 1u, never, a.timeout_ns);
     for (int i = max(0, issued_v - Geo<D>::kStages); i < issued_v; ++i)
@@ -229,21 +237,27 @@ __device__ void scan_values(Smem<D>& sm, const TileArgs& a, const Work& w, volat
             return;
         }
         if (j >= w.clean) {
+            // 0 * x is NaN for the values looked for and changes nothing else
             uint4* tile = reinterpret_cast<uint4*>(sm.v[stage]);
-            uint32_t any = 0;
-#pragma unroll 4
+            uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll 8
             for (int i = lane; i < Geo<D>::kTileBytes / 16; i += 32) {
-                uint4 x = tile[i];
-                const uint32_t b0 = nonfinite_halves<FP16>(x.x), b1 = nonfinite_halves<FP16>(x.y);
-                const uint32_t b2 = nonfinite_halves<FP16>(x.z), b3 = nonfinite_halves<FP16>(x.w);
-                if (b0 | b1 | b2 | b3) {
-                    any = 1;
-                    x.x = finite_or_zero<FP16>(x.x, b0), x.y = finite_or_zero<FP16>(x.y, b1);
-                    x.z = finite_or_zero<FP16>(x.z, b2), x.w = finite_or_zero<FP16>(x.w, b3);
+                const uint4 x = tile[i];
+                sum[0] = Half16<FP16>::add_zero_times(x.x, sum[0]), sum[1] = Half16<FP16>::add_zero_times(x.y, sum[1]);
+                sum[2] = Half16<FP16>::add_zero_times(x.z, sum[2]), sum[3] = Half16<FP16>::add_zero_times(x.w, sum[3]);
+            }
+            if (nonfinite_halves<FP16>(sum[0]) | nonfinite_halves<FP16>(sum[1]) | nonfinite_halves<FP16>(sum[2]) |
+                nonfinite_halves<FP16>(sum[3])) {
+                for (int i = lane; i < Geo<D>::kTileBytes / 16; i += 32) {
+                    uint4 x = tile[i];
+                    x.x = finite_or_zero<FP16>(x.x, nonfinite_halves<FP16>(x.x));
+                    x.y = finite_or_zero<FP16>(x.y, nonfinite_halves<FP16>(x.y));
+                    x.z = finite_or_zero<FP16>(x.z, nonfinite_halves<FP16>(x.z));
+                    x.w = finite_or_zero<FP16>(x.w, nonfinite_halves<FP16>(x.w));
                     tile[i] = x;
                 }
+                *reinterpret_cast<volatile int*>(&sm.nonfinite) = 1;
             }
-            if (any) *reinterpret_cast<volatile int*>(&sm.nonfinite) = 1;
             fence_proxy_async_shared();
         }
         __syncwarp();
@@ -550,8 +564,14 @@ __device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uin
     const int head = w.kvh * a.p.group + row % a.p.group;
     const int64_t tok = w.s.q0 + query, qh = tok * a.p.heads + head;
     const bool split = a.p.splits > 1;
-    uint16_t* dst = static_cast<uint16_t*>(a.p.o) + tok * a.p.on + head * a.p.oh;
-    float* part = split ? a.p.part_o + (w.split * a.p.total_q * a.p.heads + qh) * D : nullptr;
+    // A warp's 32 rows go out through the Q tile's shared memory (no MMA reads
+    // it any more): a thread's own row would be written 16 bytes here and 16
+    // there, whole rows take a quarter of the time.  16-byte chunks are swizzled by
+    // the row so that neither side collides.
+    constexpr int kPieces = D / 8;  // 16-byte chunks of a row of the element type
+    constexpr int kSwap = kPieces % 8 ? 3 : 7;
+    uint4* stage = reinterpret_cast<uint4*>(sm.q[t]) + quarter * 32 * kPieces;
+    const int64_t rows = a.p.total_q * a.p.heads;
 #pragma unroll 1
     for (int cc = 0; cc < Geo<D>::kChunks; ++cc) {
         uint32_t raw[32];
@@ -562,8 +582,7 @@ __device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uin
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = n > 0 && l != 0.f ? __uint_as_float(raw[i]) * inv_l : 0.f;
-        if (!in) continue;
-        if (cleared) {
+        if (cleared && in) {
             float tmp[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) tmp[i] = o[i];
@@ -573,20 +592,44 @@ __device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uin
             for (int i = 0; i < 32; ++i) o[i] = tmp[i];
         }
         if (split) {
-            float4* d4 = reinterpret_cast<float4*>(part + 32 * cc);
+            // fp32 rows, 32 channels at a time
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d4[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 8; ++i)
+                stage[lane * 8 + (i ^ (lane & 7))] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                                                                __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
+            __syncwarp();
+            float* part = a.p.part_o + static_cast<int64_t>(w.split) * rows * D + 32 * cc;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + lane / 8, c16 = lane % 8;
+                const int64_t out = __shfl_sync(0xffffffffu, qh, r);
+                const bool there = __shfl_sync(0xffffffffu, in, r);
+                if (there) reinterpret_cast<uint4*>(part + out * D)[c16] = stage[r * 8 + (c16 ^ (r & 7))];
+            }
+            __syncwarp();
         } else {
-            uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * cc);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                d4[i] = make_uint4(H::pack(o[8 * i], o[8 * i + 1]), H::pack(o[8 * i + 2], o[8 * i + 3]),
-                                   H::pack(o[8 * i + 4], o[8 * i + 5]), H::pack(o[8 * i + 6], o[8 * i + 7]));
+                stage[lane * kPieces + ((cc * 4 + i) ^ (lane & kSwap))] =
+                    make_uint4(H::pack(o[8 * i], o[8 * i + 1]), H::pack(o[8 * i + 2], o[8 * i + 3]),
+                               H::pack(o[8 * i + 4], o[8 * i + 5]), H::pack(o[8 * i + 6], o[8 * i + 7]));
+        }
+    }
+    if (!split) {
+        __syncwarp();
+        const int64_t mine = tok * a.p.on + head * a.p.oh;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int r = (i * 32 + lane) / kPieces, c16 = (i * 32 + lane) % kPieces;
+            const int64_t out = __shfl_sync(0xffffffffu, mine, r);
+            const bool there = __shfl_sync(0xffffffffu, in, r);
+            if (there)
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.p.o) + out)[c16] = stage[r * kPieces + (c16 ^ (r & kSwap))];
         }
     }
     if (in) {
         if (split)
-            a.p.part_lse[w.split * a.p.total_q * a.p.heads + qh] = lse2;
+            a.p.part_lse[w.split * rows + qh] = lse2;
         else if (a.p.lse)
             a.p.lse[qh] = lse2 * 0.6931471805599453f;
     }
