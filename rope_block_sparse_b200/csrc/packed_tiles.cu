@@ -70,6 +70,31 @@ struct Geo {
     static_assert(!kSepP || kColP + 64 <= kTmemCols, "P buffer inside the allocation");
 };
 
+// What one CTA works on.
+struct Work {
+    PackedSeq s;
+    int kvh, split;
+    int t0;        // first query of tile 0, in the sequence
+    int queries;   // queries of the sequence that count
+    int begin;     // first key of the part
+    int end0, end1;  // one past the last key any row of tile 0, 1 attends in this part
+    int n0, n1;      // 128-key steps of tile 0, 1
+    int last;        // the tile with the most steps: 1 if it exists, else 0
+    int clean;       // steps before the first in which some row does not attend some key
+    int none;        // no work
+    __device__ __forceinline__ int end(int t) const { return t ? end1 : end0; }
+    __device__ __forceinline__ int n(int t) const { return t ? n1 : n0; }
+    __device__ __forceinline__ int steps() const { return last ? n1 : n0; }
+};
+
+// What the issuing threads' loops need of it, in registers.
+struct Steps {
+    int n0, n1, last;
+    __device__ __forceinline__ explicit Steps(const Work& w) : n0(w.n0), n1(w.n1), last(w.last) {}
+    __device__ __forceinline__ int n(int t) const { return t ? n1 : n0; }
+    __device__ __forceinline__ int steps() const { return last ? n1 : n0; }
+};
+
 template <int D>
 struct Smem {
     static constexpr int kStages = Geo<D>::kStages;
@@ -83,6 +108,8 @@ struct Smem {
     uint64_t s_read[2];   // separate P: S_t has been read into registers
     uint64_t pv_done[2];  // separate P: PV_t(j) has completed (P buffer free)
     uint64_t mma_drain, pv_drain;
+    Work work;  // in shared memory: what is needed after the main loop does not sit in registers during it
+    int64_t place[8][32];  // where each softmax warp's rows go, in elements; -1: nowhere
     uint32_t tmem_base;
     int abort_flag;
     int never;      // stays 0: abort flag for waits that must ignore an abort
@@ -95,23 +122,6 @@ struct TileArgs {
     int per_tile;  // T: queries of a tile
     int* status;
     uint64_t timeout_ns;
-};
-
-// What one CTA works on.
-struct Work {
-    PackedSeq s;
-    int kvh, split;
-    int t0;        // first query of tile 0, in the sequence
-    int queries;   // queries of the sequence that count
-    int begin;     // first key of the part
-    int end0, end1;  // one past the last key any row of tile 0, 1 attends in this part
-    int n0, n1;      // 128-key steps of tile 0, 1
-    int last;        // the tile with the most steps: 1 if it exists, else 0
-    int clean;       // steps before the first in which some row does not attend some key
-    // selects, not arrays: an index known only at run time would put them in local memory
-    __device__ __forceinline__ int end(int t) const { return t ? end1 : end0; }
-    __device__ __forceinline__ int n(int t) const { return t ? n1 : n0; }
-    __device__ __forceinline__ int steps() const { return last ? n1 : n0; }
 };
 
 __device__ __forceinline__ void raise_timeout(const TileArgs& a, volatile int* abort_flag) {
@@ -136,8 +146,9 @@ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
     return idesc_bf16_f32(M, N, a_mn, b_mn) & ~(FP16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// Finds this CTA's work; false if there is none.  The whole warp takes part (the
-// search tries 32 sequences at a time: each try is a trip to memory).
+// Finds this CTA's work; false if there is none.  The whole warp takes part: 32
+// sequences are tried at a time, each with all its entries, since a trip to
+// memory is what this takes.
 __device__ __forceinline__ bool find_work(const TileArgs& a, Work& w) {
     const int lane = threadIdx.x & 31;
     uint32_t at = blockIdx.x;
@@ -146,19 +157,28 @@ __device__ __forceinline__ bool find_work(const TileArgs& a, Work& w) {
     w.kvh = at % a.p.kv_heads;
     w.split = at / a.p.kv_heads;
     const int span = 2 * a.per_tile;
-    auto first_pair = [&](int s) {
-        const int64_t q0 = min(max(static_cast<int64_t>(__ldg(a.p.starts_q + s)), int64_t(0)), a.p.total_q);
-        return static_cast<int>(q0 / span) + s;
-    };
     int lo = 0, hi = a.p.seqs;  // the last sequence in [lo, hi) whose pairs start at or before this one
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, probe = lo + (lane + 1) * step;
-        const uint32_t yes = __ballot_sync(0xffffffffu, probe < hi && first_pair(probe) <= pair);
-        lo += __popc(yes) * step;
+    PackedSeq mine;
+    int first;
+    for (;;) {
+        const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
+        mine = packed_seq(a.p, min(probe, a.p.seqs - 1));
+        first = static_cast<int>(mine.q0 / span) + probe;
+        // lane 0 stands for lo itself
+        const uint32_t yes = __ballot_sync(0xffffffffu, lane == 0 || (probe < hi && first <= pair));
+        const int winner = 31 - __clz(yes);
+        if (step == 1) {
+            w.s.q0 = __shfl_sync(0xffffffffu, mine.q0, winner);
+            w.s.k0 = __shfl_sync(0xffffffffu, mine.k0, winner);
+            w.s.lq = __shfl_sync(0xffffffffu, mine.lq, winner);
+            w.s.lk = __shfl_sync(0xffffffffu, mine.lk, winner);
+            first = __shfl_sync(0xffffffffu, first, winner);
+            break;
+        }
+        lo += winner * step;
         hi = min(hi, lo + step);
     }
-    const int64_t t0 = static_cast<int64_t>(pair - first_pair(lo)) * span;
-    w.s = packed_seq(a.p, lo);
+    const int64_t t0 = static_cast<int64_t>(pair - first) * span;
     w.queries = static_cast<int>(min(static_cast<int64_t>(w.s.lq), a.p.max_q));
     if (t0 < 0 || t0 >= w.queries) return false;
     w.t0 = static_cast<int>(t0);
@@ -185,11 +205,11 @@ template <int D>
 __device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CUtensorMap* tq, const CUtensorMap* tk,
                          const CUtensorMap* tv, volatile int* abort_flag) {
     const uint32_t q_bytes = Geo<D>::kChunks * 64u * static_cast<uint32_t>(a.per_tile * a.p.group);
-    const int q0 = static_cast<int>(w.s.q0) + w.t0, k0 = static_cast<int>(w.s.k0) + w.begin;
+    const int q0 = static_cast<int>(w.s.q0) + w.t0, k0 = static_cast<int>(w.s.k0) + w.begin, kvh = w.kvh;
     auto load_q = [&](int t) {
         mbar_arrive_expect_tx(&sm.q_full[t], q_bytes);
         for (int c = 0; c < Geo<D>::kChunks; ++c)
-            tma_load_4d(sm.q[t] + c * kChunkBytes, tq, &sm.q_full[t], 32 * c, 0, w.kvh, q0 + t * a.per_tile);
+            tma_load_4d(sm.q[t] + c * kChunkBytes, tq, &sm.q_full[t], 32 * c, 0, kvh, q0 + t * a.per_tile);
     };
     // a tile without steps needs no Q (its rows' zeros go out through that memory)
     if (w.n0 > 0) load_q(0);
@@ -201,13 +221,13 @@ __device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CU
         if (!(ok = mbar_wait(&sm.k_empty[stage], phase ^ 1u, abort_flag, a.timeout_ns))) break;
         mbar_arrive_expect_tx(&sm.k_full[stage], Geo<D>::kTileBytes);
         for (int c = 0; c < Geo<D>::kChunks; ++c)
-            tma_load_4d(sm.k[stage] + c * kChunkBytes, tk, &sm.k_full[stage], 32 * c, w.kvh, k0 + j * 128, 0);
+            tma_load_4d(sm.k[stage] + c * kChunkBytes, tk, &sm.k_full[stage], 32 * c, kvh, k0 + j * 128, 0);
         ++issued_k;
         if (j == 0 && w.n1 > 0) load_q(1);  // behind the K that the first tile waits for
         if (!(ok = mbar_wait(&sm.v_empty[stage], phase ^ 1u, abort_flag, a.timeout_ns))) break;
         mbar_arrive_expect_tx(&sm.v_full[stage], Geo<D>::kTileBytes);
         for (int c = 0; c < Geo<D>::kChunks; ++c)
-            tma_load_4d(sm.v[stage] + c * kChunkBytes, tv, &sm.v_full[stage], 32 * c, w.kvh, k0 + j * 128, 0);
+            tma_load_4d(sm.v[stage] + c * kChunkBytes, tv, &sm.v_full[stage], 32 * c, kvh, k0 + j * 128, 0);
         ++issued_v;
         if (++stage == Geo<D>::kStages) {
             stage = 0;
@@ -229,14 +249,14 @@ __device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CU
 // does not attend some key of the step.
 template <int D, bool FP16>
 __device__ void scan_values(Smem<D>& sm, const TileArgs& a, const Work& w, volatile int* abort_flag) {
-    const int lane = threadIdx.x & 31, n = w.steps();
+    const int lane = threadIdx.x & 31, n = w.steps(), clean = w.clean;
     uint32_t stage = 0, phase = 0;
     for (int j = 0; j < n; ++j) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.v_full[stage], phase, abort_flag, a.timeout_ns))) {
             if (lane == 0) raise_timeout(a, abort_flag);
             return;
         }
-        if (j >= w.clean) {
+        if (j >= clean) {
             // 0 * x is NaN for the values looked for and changes nothing else
             uint4* tile = reinterpret_cast<uint4*>(sm.v[stage]);
             uint32_t sum[4] = {0, 0, 0, 0};
@@ -275,7 +295,7 @@ struct MmaState {
 
 // S_t(j) = Q_t K(j)^T.  The first tile of a step waits for K, the last one releases it.
 template <int D, bool FP16>
-__device__ __forceinline__ bool issue_qk(Smem<D>& sm, const TileArgs& a, const Work& w, const MmaState& st,
+__device__ __forceinline__ bool issue_qk(Smem<D>& sm, const TileArgs& a, const Steps& w, const MmaState& st,
                                          uint32_t tmem, int t, int j, volatile int* abort_flag) {
     const uint32_t stage = static_cast<uint32_t>(j) % Geo<D>::kStages, phase = (static_cast<uint32_t>(j) / Geo<D>::kStages) & 1u;
     if (!mbar_wait(&sm.k_full[stage], phase, abort_flag, a.timeout_ns)) return false;
@@ -292,7 +312,7 @@ __device__ __forceinline__ bool issue_qk(Smem<D>& sm, const TileArgs& a, const W
 
 // O_t += P_t(j) V(j).
 template <int D, bool FP16>
-__device__ __forceinline__ bool issue_pv(Smem<D>& sm, const TileArgs& a, const Work& w, const MmaState& st,
+__device__ __forceinline__ bool issue_pv(Smem<D>& sm, const TileArgs& a, const Steps& w, const MmaState& st,
                                          uint32_t tmem, int t, int j, volatile int* abort_flag) {
     const uint32_t stage = static_cast<uint32_t>(j) % Geo<D>::kStages, phase = (static_cast<uint32_t>(j) / Geo<D>::kStages) & 1u;
     if (!mbar_wait(&sm.v_ready[stage], phase, abort_flag, a.timeout_ns)) return false;
@@ -309,7 +329,8 @@ __device__ __forceinline__ bool issue_pv(Smem<D>& sm, const TileArgs& a, const W
 
 // Separate P: QK^T and PV touch disjoint TMEM and have a thread each.
 template <int D, bool FP16>
-__device__ void qk_issuer(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_t tmem, volatile int* abort_flag) {
+__device__ void qk_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint32_t tmem, volatile int* abort_flag) {
+    const Steps w(work);
     if (w.steps() == 0) return;
     MmaState st;
     st.dq0 = kmajor_base(sm.q[0]);
@@ -332,7 +353,8 @@ __device__ void qk_issuer(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_
 }
 
 template <int D, bool FP16>
-__device__ void pv_issuer(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_t tmem, volatile int* abort_flag) {
+__device__ void pv_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint32_t tmem, volatile int* abort_flag) {
+    const Steps w(work);
     if (w.steps() == 0) return;
     MmaState st;
     st.dv = mnmajor_base(sm.v[0]);
@@ -356,7 +378,8 @@ __device__ void pv_issuer(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_
 // P over S: one thread, PV_t(j) then QK_t(j+1) per tile (the QK overwrites the
 // columns the PV reads; MMAs of one thread complete in issue order).
 template <int D, bool FP16>
-__device__ void mma_issuer(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_t tmem, volatile int* abort_flag) {
+__device__ void mma_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint32_t tmem, volatile int* abort_flag) {
+    const Steps w(work);
     if (w.steps() == 0) return;
     MmaState st;
     st.dq0 = kmajor_base(sm.q[0]);
@@ -431,7 +454,7 @@ __device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uin
     const uint32_t tS = tmem + lane_addr + col_s(t);
     const uint32_t tO = tmem + lane_addr + Geo<D>::col_o(t);
     const uint32_t tP = tmem + lane_addr + Geo<D>::kColP;
-    const int n = w.n(t);
+    const int n = w.n(t), n0 = w.n0, last = w.last;
     const int query = w.t0 + t * a.per_tile + row / a.p.group;
     const bool in = row < a.per_tile * a.p.group && query < w.queries;
     // rows that are no query's see what the tile sees (and are not written), so
@@ -444,7 +467,7 @@ __device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uin
     // step j - 1.  It was issued after PV_t(j-1), so O_t is stable too.  The
     // wait names a phase at most one ahead of the barrier's last completed one.
     auto wait_p_buffer = [&](int j) -> bool {
-        const bool other = t == 0 ? w.last == 1 : j < w.n0;
+        const bool other = t == 0 ? last == 1 : j < n0;
         const int u = other ? 1 - t : t;
         const int ph = other && t == 1 ? j : j - 1;
         if (ph < 0) return true;
@@ -565,67 +588,77 @@ __device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uin
     const int64_t tok = w.s.q0 + query, qh = tok * a.p.heads + head;
     const bool split = a.p.splits > 1;
     // A warp's 32 rows go out through the Q tile's shared memory (no MMA reads
-    // it any more): a thread's own row would be written 16 bytes here and 16
-    // there, whole rows take a quarter of the time.  16-byte chunks are swizzled by
-    // the row so that neither side collides.
+    // it any more) as whole rows: a thread's own row would be written 16 bytes
+    // here and 16 there.  16-byte chunks are swizzled by the row so that neither
+    // side collides.
+    const int64_t rows = a.p.total_q * a.p.heads;
+    int64_t* places = sm.place[t * 4 + quarter];
+    places[lane] = !in ? -1 : split ? (w.split * rows + qh) * D : tok * a.p.on + head * a.p.oh;
+    uint4* stage = reinterpret_cast<uint4*>(sm.q[t]) + quarter * 32 * (D / 8);
     constexpr int kPieces = D / 8;  // 16-byte chunks of a row of the element type
     constexpr int kSwap = kPieces % 8 ? 3 : 7;
-    uint4* stage = reinterpret_cast<uint4*>(sm.q[t]) + quarter * 32 * kPieces;
-    const int64_t rows = a.p.total_q * a.p.heads;
-#pragma unroll 1
-    for (int cc = 0; cc < Geo<D>::kChunks; ++cc) {
-        uint32_t raw[32];
-        float o[32];
-        if (n > 0) {
-            tmem_ld_x32(tO + 32u * cc, raw);
-            tmem_wait_ld_x32(raw);
-        }
+    uint32_t x[D];
+    if (n > 0) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = n > 0 && l != 0.f ? __uint_as_float(raw[i]) * inv_l : 0.f;
-        if (cleared && in) {
+        for (int cc = 0; cc < Geo<D>::kChunks; ++cc) tmem_ld_x32(tO + 32u * cc, slice32(x + 32 * cc));
+#pragma unroll
+        for (int cc = 0; cc < Geo<D>::kChunks; ++cc) tmem_wait_ld_x32(slice32(x + 32 * cc));
+    }
+    const bool keys = n > 0 && l != 0.f;
+#pragma unroll
+    for (int i = 0; i < D; ++i) x[i] = keys ? __float_as_uint(__uint_as_float(x[i]) * inv_l) : 0u;
+    if (cleared && in) {
+#pragma unroll
+        for (int cc = 0; cc < Geo<D>::kChunks; ++cc) {
             float tmp[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) tmp[i] = o[i];
+            for (int i = 0; i < 32; ++i) tmp[i] = __uint_as_float(x[32 * cc + i]);
             add_nonfinite<FP16>(tmp, static_cast<const uint16_t*>(a.p.v) + w.s.k0 * a.p.vn + w.kvh * a.p.vh + 32 * cc, a.p.vn,
                                 w.begin + 128 * w.clean, limit);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = tmp[i];
-        }
-        if (split) {
-            // fp32 rows, 32 channels at a time
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                stage[lane * 8 + (i ^ (lane & 7))] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
-                                                                __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
-            __syncwarp();
-            float* part = a.p.part_o + static_cast<int64_t>(w.split) * rows * D + 32 * cc;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = i * 4 + lane / 8, c16 = lane % 8;
-                const int64_t out = __shfl_sync(0xffffffffu, qh, r);
-                const bool there = __shfl_sync(0xffffffffu, in, r);
-                if (there) reinterpret_cast<uint4*>(part + out * D)[c16] = stage[r * 8 + (c16 ^ (r & 7))];
-            }
-            __syncwarp();
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                stage[lane * kPieces + ((cc * 4 + i) ^ (lane & kSwap))] =
-                    make_uint4(H::pack(o[8 * i], o[8 * i + 1]), H::pack(o[8 * i + 2], o[8 * i + 3]),
-                               H::pack(o[8 * i + 4], o[8 * i + 5]), H::pack(o[8 * i + 6], o[8 * i + 7]));
+            for (int i = 0; i < 32; ++i) x[32 * cc + i] = __float_as_uint(tmp[i]);
         }
     }
-    if (!split) {
-        __syncwarp();
-        const int64_t mine = tok * a.p.on + head * a.p.oh;
+    // rows [lane / per, + 32 / per, ...) of the staged chunks, `per` lanes a row
+    auto out = [&](auto* base, int pieces, int swap, int first_channel) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint4 v[kPieces / 2];
+            int64_t at[kPieces / 2];
+#pragma unroll
+            for (int i = 0; i < kPieces / 2; ++i) {
+                const int piece = (half * (kPieces / 2) + i) * 32 + lane, r = piece / pieces, c = piece % pieces;
+                v[i] = stage[r * pieces + (c ^ (r & swap))];
+                at[i] = places[r];
+                if (at[i] >= 0) at[i] += first_channel + c * (16 / static_cast<int>(sizeof(*base)));
+            }
+#pragma unroll
+            for (int i = 0; i < kPieces / 2; ++i)
+                if (at[i] >= 0) *reinterpret_cast<uint4*>(base + at[i]) = v[i];
+        }
+    };
+    if (split) {
+        // fp32 rows, half of the channels at a time
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int c = h * (D / 2) + 4 * i;
+                stage[lane * kPieces + (i ^ (lane & kSwap))] = make_uint4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+            }
+            __syncwarp();
+            out(a.p.part_o, kPieces, kSwap, h * (D / 2));
+            __syncwarp();
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int r = (i * 32 + lane) / kPieces, c16 = (i * 32 + lane) % kPieces;
-            const int64_t out = __shfl_sync(0xffffffffu, mine, r);
-            const bool there = __shfl_sync(0xffffffffu, in, r);
-            if (there)
-                reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.p.o) + out)[c16] = stage[r * kPieces + (c16 ^ (r & kSwap))];
+            auto f = [&](int e) { return __uint_as_float(x[8 * i + e]); };
+            stage[lane * kPieces + (i ^ (lane & kSwap))] =
+                make_uint4(H::pack(f(0), f(1)), H::pack(f(2), f(3)), H::pack(f(4), f(5)), H::pack(f(6), f(7)));
         }
+        __syncwarp();
+        out(static_cast<uint16_t*>(a.p.o), kPieces, kSwap, 0);
     }
     if (in) {
         if (split)
@@ -642,10 +675,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw + (((base + 1023u) & ~1023u) - base));
-    Work w;
-    if (!find_work(a, w)) return;
-
     const int warp = threadIdx.x >> 5;
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.q_full[t], 1);
@@ -674,17 +708,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensor_map(&tk);
         prefetch_tensor_map(&tv);
     }
-    if (warp == kMmaWarp) {
-        tmem_alloc(&sm.tmem_base, kTmemCols);
-        tmem_relinquish();
+    {
+        Work mine;
+        mine.none = !find_work(a, mine);
+        if (threadIdx.x == 0) sm.work = mine;
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    const Work& w = sm.work;
     const uint32_t tmem = sm.tmem_base;
     volatile int* abort_flag = &sm.abort_flag;
 
-    if (warp < kSoftmaxWarps) {
+    if (w.none) {
+        // nothing to do
+    } else if (warp < kSoftmaxWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int t = warp >> 2;
         if (t <= w.last) softmax_group<D, FP16>(sm, a, w, tmem, t, abort_flag);
