@@ -242,7 +242,7 @@ h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, size_t* rows
         return H3A_ERR_INVALID_ARG;
     *plan = packed_plan(*d);
     const int group = d->heads / d->kv_heads;
-    const double columns = plan->tiles ? static_cast<double>(packed_tile_pairs(d->total_q, d->seqs, group)) : d->seqs;
+    const double columns = plan->tiles ? static_cast<double>(packed_tile_groups(d->total_q, d->seqs, group, plan->tiles)) : d->seqs;
     const double grid = columns * d->kv_heads * plan->splits;
     const double rows = static_cast<double>(d->total_q) * d->heads;
     if (grid >= static_cast<double>(lim) || rows >= 4.0 * static_cast<double>(lim)) return H3A_ERR_UNSUPPORTED;
@@ -595,7 +595,7 @@ h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, con
         CUtensorMap tq, tk, tv;
         e = make_packed_tensor_maps(*d, q, k, v, &tq, &tk, &tv);
         if (e == cudaSuccess)
-            e = launch_packed_tiles(tq, tk, tv, a, d->head_dim, d->dtype == H3A_FP16, status, kWaitLimitNs, st);
+            e = launch_packed_tiles(tq, tk, tv, a, d->head_dim, d->dtype == H3A_FP16, plan.tiles, status, kWaitLimitNs, st);
     } else {
         e = launch_packed_rows(a, d->head_dim, d->dtype == H3A_FP16, st);
     }

@@ -5,6 +5,9 @@
 
 #include "prompt_internal.h"
 
+#ifndef ONE_TILE_KEYS
+#define ONE_TILE_KEYS 1024
+#endif
 namespace h3a {
 
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
@@ -20,8 +23,8 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
 
 int packed_queries_per_tile(int group) { return 128 / group; }
 
-int64_t packed_tile_pairs(int64_t total_q, int seqs, int group) {
-    return total_q / (2 * packed_queries_per_tile(group)) + seqs;
+int64_t packed_tile_groups(int64_t total_q, int seqs, int group, int tiles) {
+    return total_q / (tiles * packed_queries_per_tile(group)) + seqs;
 }
 
 PackedPlan packed_plan(const h3a_packed_desc& d) {
@@ -31,7 +34,7 @@ PackedPlan packed_plan(const h3a_packed_desc& d) {
     // Up to 16 rows (queries x heads of a group) fit one mma.m16n8k16 tile of
     // the row kernel, which then reads the keys once; more go to the 128-row
     // tiles of the tcgen05 kernel.
-    p.tiles = max_q * group > 16;
+    p.tiles = max_q * group <= 16 ? 0 : max_k <= ONE_TILE_KEYS ? 1 : 2;
     int64_t splits, chunk;
     if (p.tiles) {
         // a part for every multiprocessor without work, each of at least 512

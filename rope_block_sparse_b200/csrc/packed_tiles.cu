@@ -44,30 +44,35 @@
 namespace h3a {
 namespace {
 
-constexpr int kSoftmaxWarps = 8;  // 2 warpgroups: one per query tile
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kPvWarp = 10, kScanWarp = 11;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
-// Register split (setmaxnreg): the softmax warpgroups hold a 128-value row each.
-constexpr uint32_t kRegsLaunch = (65536 / kThreads) / 8 * 8;
-constexpr uint32_t kRegsSoftmax = 200, kRegsOther = 80;
-static_assert(kSoftmaxWarps * 32 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
 constexpr int kChunkBytes = 128 * 64;  // 128 rows x 32 channels, 64-byte swizzle
-constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSwizzle64 = 4;
 __host__ __device__ constexpr uint32_t col_s(int t) { return t ? 128u : 0u; }
 
-template <int D>
+// A CTA of TILES query tiles, by head dimension.  Two tiles share every K and V
+// tile and hide each other's softmax: one CTA a multiprocessor.  One tile is
+// half of everything, so that two CTAs fit and hide each other's beginning and
+// end, which is what short sequences consist of.
+template <int D_, int TILES>
 struct Geo {
+    static constexpr int D = D_, kTiles = TILES;
+    static constexpr int kSoftmaxWarps = 4 * TILES;  // a warpgroup per query tile
+    static constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1, kPvWarp = kSoftmaxWarps + 2;
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+    static constexpr int kCtas = TILES == 1 ? 2 : 1;  // per multiprocessor
+    // Register split (setmaxnreg): the softmax warpgroups hold a 128-value row each.
+    static constexpr uint32_t kRegsLaunch = (65536 / kCtas / kThreads) / 8 * 8;
+    static constexpr uint32_t kRegsSoftmax = 200, kRegsOther = TILES == 1 ? 56 : 80;
+    static_assert(kSoftmaxWarps * 32 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
     static constexpr int kChunks = D / 32;
     static constexpr int kTileBytes = kChunks * kChunkBytes;
-    static constexpr int kStages = D == 64 ? 5 : D == 96 ? 3 : 2;
+    static constexpr int kStages = TILES == 1 ? (D == 64 ? 2 : 1) : D == 64 ? 5 : D == 96 ? 3 : 2;
     static constexpr int kKSteps = D / 16;
-    __host__ __device__ static constexpr uint32_t col_o(int t) { return 256u + (t ? D : 0); }
-    // Up to D = 96 a P buffer of 64 columns stands behind O_1 and the tiles take
-    // it in turn; at D = 128 P_t is written over S_t.
-    static constexpr bool kSepP = D <= 96;
-    static constexpr uint32_t kColP = 256u + 2 * D;
-    static_assert(!kSepP || kColP + 64 <= kTmemCols, "P buffer inside the allocation");
+    // TMEM: S_0 (S_1), O_0 (O_1), and where it fits a P buffer of 64 columns that
+    // the tiles take in turn; else P_t is written over S_t.
+    static constexpr uint32_t kTmemCols = 256 * TILES;
+    __host__ __device__ static constexpr uint32_t col_o(int t) { return 128u * TILES + (t ? D : 0); }
+    static constexpr uint32_t kColP = 128u * TILES + TILES * D;
+    static constexpr bool kSepP = kColP + 64 <= kTmemCols;
 };
 
 // What one CTA works on.
@@ -95,12 +100,12 @@ struct Steps {
     __device__ __forceinline__ int steps() const { return last ? n1 : n0; }
 };
 
-template <int D>
+template <class G>
 struct Smem {
-    static constexpr int kStages = Geo<D>::kStages;
-    uint8_t q[2][Geo<D>::kTileBytes];
-    uint8_t k[kStages][Geo<D>::kTileBytes];
-    uint8_t v[kStages][Geo<D>::kTileBytes];
+    static constexpr int kStages = G::kStages;
+    uint8_t q[G::kTiles][G::kTileBytes];
+    uint8_t k[kStages][G::kTileBytes];
+    uint8_t v[kStages][G::kTileBytes];
     uint64_t q_full[2];
     uint64_t k_full[kStages], k_empty[kStages];
     uint64_t v_full[kStages], v_ready[kStages], v_empty[kStages];
@@ -109,7 +114,7 @@ struct Smem {
     uint64_t pv_done[2];  // separate P: PV_t(j) has completed (P buffer free)
     uint64_t mma_drain, pv_drain;
     Work work;  // in shared memory: what is needed after the main loop does not sit in registers during it
-    int64_t place[8][32];  // where each softmax warp's rows go, in elements; -1: nowhere
+    int64_t place[G::kSoftmaxWarps][32];  // where each softmax warp's rows go, in elements; -1: nowhere
     uint32_t tmem_base;
     int abort_flag;
     int never;      // stays 0: abort flag for waits that must ignore an abort
@@ -149,14 +154,14 @@ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
 // Finds this CTA's work; false if there is none.  The whole warp takes part: 32
 // sequences are tried at a time, each with all its entries, since a trip to
 // memory is what this takes.
-__device__ __forceinline__ bool find_work(const TileArgs& a, Work& w) {
+__device__ __forceinline__ bool find_work(const TileArgs& a, int tiles, Work& w) {
     const int lane = threadIdx.x & 31;
     uint32_t at = blockIdx.x;
     const int pair = a.pairs - 1 - static_cast<int>(at % a.pairs);
     at /= a.pairs;
     w.kvh = at % a.p.kv_heads;
     w.split = at / a.p.kv_heads;
-    const int span = 2 * a.per_tile;
+    const int span = tiles * a.per_tile;
     int lo = 0, hi = a.p.seqs;  // the last sequence in [lo, hi) whose pairs start at or before this one
     PackedSeq mine;
     int first;
@@ -182,7 +187,7 @@ __device__ __forceinline__ bool find_work(const TileArgs& a, Work& w) {
     w.queries = static_cast<int>(min(static_cast<int64_t>(w.s.lq), a.p.max_q));
     if (t0 < 0 || t0 >= w.queries) return false;
     w.t0 = static_cast<int>(t0);
-    w.last = w.t0 + a.per_tile < w.queries ? 1 : 0;
+    w.last = tiles == 2 && w.t0 + a.per_tile < w.queries ? 1 : 0;
     w.begin = 0;
     w.end1 = w.n1 = 0;
     for (int t = 0; t <= w.last; ++t) {
@@ -201,14 +206,14 @@ __device__ __forceinline__ bool find_work(const TileArgs& a, Work& w) {
     return w.split == 0 || w.steps() > 0;
 }
 
-template <int D>
-__device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CUtensorMap* tq, const CUtensorMap* tk,
+template <class G>
+__device__ void producer(Smem<G>& sm, const TileArgs& a, const Work& w, const CUtensorMap* tq, const CUtensorMap* tk,
                          const CUtensorMap* tv, volatile int* abort_flag) {
-    const uint32_t q_bytes = Geo<D>::kChunks * 64u * static_cast<uint32_t>(a.per_tile * a.p.group);
+    const uint32_t q_bytes = G::kChunks * 64u * static_cast<uint32_t>(a.per_tile * a.p.group);
     const int q0 = static_cast<int>(w.s.q0) + w.t0, k0 = static_cast<int>(w.s.k0) + w.begin, kvh = w.kvh;
     auto load_q = [&](int t) {
         mbar_arrive_expect_tx(&sm.q_full[t], q_bytes);
-        for (int c = 0; c < Geo<D>::kChunks; ++c)
+        for (int c = 0; c < G::kChunks; ++c)
             tma_load_4d(sm.q[t] + c * kChunkBytes, tq, &sm.q_full[t], 32 * c, 0, kvh, q0 + t * a.per_tile);
     };
     // a tile without steps needs no Q (its rows' zeros go out through that memory)
@@ -219,17 +224,17 @@ __device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CU
     int issued_k = 0, issued_v = 0;
     for (int j = 0; j < n; ++j) {
         if (!(ok = mbar_wait(&sm.k_empty[stage], phase ^ 1u, abort_flag, a.timeout_ns))) break;
-        mbar_arrive_expect_tx(&sm.k_full[stage], Geo<D>::kTileBytes);
-        for (int c = 0; c < Geo<D>::kChunks; ++c)
+        mbar_arrive_expect_tx(&sm.k_full[stage], G::kTileBytes);
+        for (int c = 0; c < G::kChunks; ++c)
             tma_load_4d(sm.k[stage] + c * kChunkBytes, tk, &sm.k_full[stage], 32 * c, kvh, k0 + j * 128, 0);
         ++issued_k;
         if (j == 0 && w.n1 > 0) load_q(1);  // behind the K that the first tile waits for
         if (!(ok = mbar_wait(&sm.v_empty[stage], phase ^ 1u, abort_flag, a.timeout_ns))) break;
-        mbar_arrive_expect_tx(&sm.v_full[stage], Geo<D>::kTileBytes);
-        for (int c = 0; c < Geo<D>::kChunks; ++c)
+        mbar_arrive_expect_tx(&sm.v_full[stage], G::kTileBytes);
+        for (int c = 0; c < G::kChunks; ++c)
             tma_load_4d(sm.v[stage] + c * kChunkBytes, tv, &sm.v_full[stage], 32 * c, kvh, k0 + j * 128, 0);
         ++issued_v;
-        if (++stage == Geo<D>::kStages) {
+        if (++stage == G::kStages) {
             stage = 0;
             phase ^= 1u;
         }
@@ -239,16 +244,16 @@ __device__ void producer(Smem<D>& sm, const TileArgs& a, const Work& w, const CU
     volatile int* never = &sm.never;
     if (w.n0 > 0) mbar_wait(&sm.q_full[0], 0u, never, a.timeout_ns);
     if (issued_k > 0 && w.n1 > 0) mbar_wait(&sm.q_full[1], 0u, never, a.timeout_ns);
-    for (int i = max(0, issued_k - Geo<D>::kStages); i < issued_k; ++i)
-        mbar_wait(&sm.k_full[i % Geo<D>::kStages], (i / Geo<D>::kStages) & 1u, never, a.timeout_ns);
-    for (int i = max(0, issued_v - Geo<D>::kStages); i < issued_v; ++i)
-        mbar_wait(&sm.v_full[i % Geo<D>::kStages], (i / Geo<D>::kStages) & 1u, never, a.timeout_ns);
+    for (int i = max(0, issued_k - G::kStages); i < issued_k; ++i)
+        mbar_wait(&sm.k_full[i % G::kStages], (i / G::kStages) & 1u, never, a.timeout_ns);
+    for (int i = max(0, issued_v - G::kStages); i < issued_v; ++i)
+        mbar_wait(&sm.v_full[i % G::kStages], (i / G::kStages) & 1u, never, a.timeout_ns);
 }
 
 // Warp 11: passes each V tile on, cleared of infinities and NaN where some row
 // does not attend some key of the step.
-template <int D, bool FP16>
-__device__ void scan_values(Smem<D>& sm, const TileArgs& a, const Work& w, volatile int* abort_flag) {
+template <class G, bool FP16>
+__device__ void scan_values(Smem<G>& sm, const TileArgs& a, const Work& w, volatile int* abort_flag) {
     const int lane = threadIdx.x & 31, n = w.steps(), clean = w.clean;
     uint32_t stage = 0, phase = 0;
     for (int j = 0; j < n; ++j) {
@@ -261,14 +266,14 @@ __device__ void scan_values(Smem<D>& sm, const TileArgs& a, const Work& w, volat
             uint4* tile = reinterpret_cast<uint4*>(sm.v[stage]);
             uint32_t sum[4] = {0, 0, 0, 0};
 #pragma unroll 8
-            for (int i = lane; i < Geo<D>::kTileBytes / 16; i += 32) {
+            for (int i = lane; i < G::kTileBytes / 16; i += 32) {
                 const uint4 x = tile[i];
                 sum[0] = Half16<FP16>::add_zero_times(x.x, sum[0]), sum[1] = Half16<FP16>::add_zero_times(x.y, sum[1]);
                 sum[2] = Half16<FP16>::add_zero_times(x.z, sum[2]), sum[3] = Half16<FP16>::add_zero_times(x.w, sum[3]);
             }
             if (nonfinite_halves<FP16>(sum[0]) | nonfinite_halves<FP16>(sum[1]) | nonfinite_halves<FP16>(sum[2]) |
                 nonfinite_halves<FP16>(sum[3])) {
-                for (int i = lane; i < Geo<D>::kTileBytes / 16; i += 32) {
+                for (int i = lane; i < G::kTileBytes / 16; i += 32) {
                     uint4 x = tile[i];
                     x.x = finite_or_zero<FP16>(x.x, nonfinite_halves<FP16>(x.x));
                     x.y = finite_or_zero<FP16>(x.y, nonfinite_halves<FP16>(x.y));
@@ -282,7 +287,7 @@ __device__ void scan_values(Smem<D>& sm, const TileArgs& a, const Work& w, volat
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.v_ready[stage]);
-        if (++stage == Geo<D>::kStages) {
+        if (++stage == G::kStages) {
             stage = 0;
             phase ^= 1u;
         }
@@ -294,32 +299,32 @@ struct MmaState {
 };
 
 // S_t(j) = Q_t K(j)^T.  The first tile of a step waits for K, the last one releases it.
-template <int D, bool FP16>
-__device__ __forceinline__ bool issue_qk(Smem<D>& sm, const TileArgs& a, const Steps& w, const MmaState& st,
+template <class G, bool FP16>
+__device__ __forceinline__ bool issue_qk(Smem<G>& sm, const TileArgs& a, const Steps& w, const MmaState& st,
                                          uint32_t tmem, int t, int j, volatile int* abort_flag) {
-    const uint32_t stage = static_cast<uint32_t>(j) % Geo<D>::kStages, phase = (static_cast<uint32_t>(j) / Geo<D>::kStages) & 1u;
+    const uint32_t stage = static_cast<uint32_t>(j) % G::kStages, phase = (static_cast<uint32_t>(j) / G::kStages) & 1u;
     if (!mbar_wait(&sm.k_full[stage], phase, abort_flag, a.timeout_ns)) return false;
     tc_fence_after_sync();
     constexpr uint32_t id = idesc<FP16>(128, 128, 0, 0);
-    const uint64_t dq = t ? st.dq1 : st.dq0, dk = st.dk + stage * (Geo<D>::kTileBytes >> 4);
+    const uint64_t dq = t ? st.dq1 : st.dq0, dk = st.dk + stage * (G::kTileBytes >> 4);
     const uint32_t d = tmem + col_s(t);
 #pragma unroll
-    for (int s = 0; s < Geo<D>::kKSteps; ++s) mma_ss(d, dq + kmajor_step(s), dk + kmajor_step(s), id, s > 0 ? 1u : 0u);
+    for (int s = 0; s < G::kKSteps; ++s) mma_ss(d, dq + kmajor_step(s), dk + kmajor_step(s), id, s > 0 ? 1u : 0u);
     tc_commit(&sm.s_full[t]);
     if (t == w.last) tc_commit(&sm.k_empty[stage]);
     return true;
 }
 
 // O_t += P_t(j) V(j).
-template <int D, bool FP16>
-__device__ __forceinline__ bool issue_pv(Smem<D>& sm, const TileArgs& a, const Steps& w, const MmaState& st,
+template <class G, bool FP16>
+__device__ __forceinline__ bool issue_pv(Smem<G>& sm, const TileArgs& a, const Steps& w, const MmaState& st,
                                          uint32_t tmem, int t, int j, volatile int* abort_flag) {
-    const uint32_t stage = static_cast<uint32_t>(j) % Geo<D>::kStages, phase = (static_cast<uint32_t>(j) / Geo<D>::kStages) & 1u;
+    const uint32_t stage = static_cast<uint32_t>(j) % G::kStages, phase = (static_cast<uint32_t>(j) / G::kStages) & 1u;
     if (!mbar_wait(&sm.v_ready[stage], phase, abort_flag, a.timeout_ns)) return false;
     tc_fence_after_sync();
-    constexpr uint32_t id = idesc<FP16>(128, D, 0, 1);
-    const uint64_t dv = st.dv + stage * (Geo<D>::kTileBytes >> 4);
-    const uint32_t d = tmem + Geo<D>::col_o(t), pa = tmem + (Geo<D>::kSepP ? Geo<D>::kColP : col_s(t));
+    constexpr uint32_t id = idesc<FP16>(128, G::D, 0, 1);
+    const uint64_t dv = st.dv + stage * (G::kTileBytes >> 4);
+    const uint32_t d = tmem + G::col_o(t), pa = tmem + (G::kSepP ? G::kColP : col_s(t));
     mma_ts(d, pa, dv, id, j > 0 ? 1u : 0u);
 #pragma unroll
     for (int s = 1; s < 8; ++s) mma_ts(d, pa + 8 * s, dv + mnmajor_step(s), id, 1u);
@@ -328,13 +333,13 @@ __device__ __forceinline__ bool issue_pv(Smem<D>& sm, const TileArgs& a, const S
 }
 
 // Separate P: QK^T and PV touch disjoint TMEM and have a thread each.
-template <int D, bool FP16>
-__device__ void qk_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint32_t tmem, volatile int* abort_flag) {
+template <class G, bool FP16>
+__device__ void qk_issuer(Smem<G>& sm, const TileArgs& a, const Work& work, uint32_t tmem, volatile int* abort_flag) {
     const Steps w(work);
     if (w.steps() == 0) return;
     MmaState st;
     st.dq0 = kmajor_base(sm.q[0]);
-    st.dq1 = kmajor_base(sm.q[1]);
+    st.dq1 = kmajor_base(sm.q[G::kTiles - 1]);
     st.dk = kmajor_base(sm.k[0]);
     bool ok = true;
     for (int j = 0; j < w.steps() && ok; ++j)
@@ -344,7 +349,7 @@ __device__ void qk_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint
                         : mbar_wait(&sm.s_read[t], static_cast<uint32_t>((j - 1) & 1), abort_flag, a.timeout_ns);
             if (!ok) break;
             tc_fence_after_sync();
-            ok = issue_qk<D, FP16>(sm, a, w, st, tmem, t, j, abort_flag);
+            ok = issue_qk<G, FP16>(sm, a, w, st, tmem, t, j, abort_flag);
         }
     if (!ok) raise_timeout(a, abort_flag);
     // Drain: every MMA this thread issued must have completed before TMEM is released.
@@ -352,8 +357,8 @@ __device__ void qk_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint
     mbar_wait(&sm.mma_drain, 0u, &sm.never, a.timeout_ns);
 }
 
-template <int D, bool FP16>
-__device__ void pv_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint32_t tmem, volatile int* abort_flag) {
+template <class G, bool FP16>
+__device__ void pv_issuer(Smem<G>& sm, const TileArgs& a, const Work& work, uint32_t tmem, volatile int* abort_flag) {
     const Steps w(work);
     if (w.steps() == 0) return;
     MmaState st;
@@ -365,7 +370,7 @@ __device__ void pv_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint
             ok = mbar_wait(&sm.p_full[t], static_cast<uint32_t>(j & 1), abort_flag, a.timeout_ns);
             if (!ok) break;
             tc_fence_after_sync();
-            ok = issue_pv<D, FP16>(sm, a, w, st, tmem, t, j, abort_flag);
+            ok = issue_pv<G, FP16>(sm, a, w, st, tmem, t, j, abort_flag);
             if (!ok) break;
             tc_commit(&sm.pv_done[t]);
             if (j + 1 == w.n(t)) tc_commit(&sm.o_done[t]);
@@ -377,29 +382,29 @@ __device__ void pv_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint
 
 // P over S: one thread, PV_t(j) then QK_t(j+1) per tile (the QK overwrites the
 // columns the PV reads; MMAs of one thread complete in issue order).
-template <int D, bool FP16>
-__device__ void mma_issuer(Smem<D>& sm, const TileArgs& a, const Work& work, uint32_t tmem, volatile int* abort_flag) {
+template <class G, bool FP16>
+__device__ void mma_issuer(Smem<G>& sm, const TileArgs& a, const Work& work, uint32_t tmem, volatile int* abort_flag) {
     const Steps w(work);
     if (w.steps() == 0) return;
     MmaState st;
     st.dq0 = kmajor_base(sm.q[0]);
-    st.dq1 = kmajor_base(sm.q[1]);
+    st.dq1 = kmajor_base(sm.q[G::kTiles - 1]);
     st.dk = kmajor_base(sm.k[0]);
     st.dv = mnmajor_base(sm.v[0]);
     bool ok = true;
     for (int t = 0; t <= w.last && ok; ++t)
         if (w.n(t) > 0)
-            ok = mbar_wait(&sm.q_full[t], 0u, abort_flag, a.timeout_ns) && issue_qk<D, FP16>(sm, a, w, st, tmem, t, 0, abort_flag);
+            ok = mbar_wait(&sm.q_full[t], 0u, abort_flag, a.timeout_ns) && issue_qk<G, FP16>(sm, a, w, st, tmem, t, 0, abort_flag);
     for (int j = 0; j < w.steps() && ok; ++j)
         for (int t = 0; t <= w.last && ok; ++t) {
             if (j >= w.n(t)) continue;
             ok = mbar_wait(&sm.p_full[t], static_cast<uint32_t>(j & 1), abort_flag, a.timeout_ns);
             if (!ok) break;
             tc_fence_after_sync();
-            ok = issue_pv<D, FP16>(sm, a, w, st, tmem, t, j, abort_flag);
+            ok = issue_pv<G, FP16>(sm, a, w, st, tmem, t, j, abort_flag);
             if (!ok) break;
             if (j + 1 < w.n(t))
-                ok = issue_qk<D, FP16>(sm, a, w, st, tmem, t, j + 1, abort_flag);
+                ok = issue_qk<G, FP16>(sm, a, w, st, tmem, t, j + 1, abort_flag);
             else
                 tc_commit(&sm.o_done[t]);
         }
@@ -412,10 +417,10 @@ __device__ __forceinline__ uint32_t (&slice32(uint32_t* x))[32] { return *reinte
 __device__ __forceinline__ uint32_t (&slice16(uint32_t* x))[16] { return *reinterpret_cast<uint32_t(*)[16]>(x); }
 
 // O row *= alpha.  Out of line: it runs only when a row's maximum grew by more than 2^8.
-template <int D>
+template <class G>
 __device__ __noinline__ void rescale_o(uint32_t tO, float alpha) {
 #pragma unroll 1
-    for (int cc = 0; cc < Geo<D>::kChunks; ++cc) {
+    for (int cc = 0; cc < G::kChunks; ++cc) {
         uint32_t o[32];
         tmem_ld_x32(tO + 32u * cc, o);
         tmem_wait_ld_x32(o);
@@ -443,17 +448,18 @@ __device__ __noinline__ void add_nonfinite(float* o, const uint16_t* v, int64_t 
 }
 
 // Softmax of query tile t: thread r owns row r (TMEM lane r), all 128 keys of a step.
-template <int D, bool FP16>
-__device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uint32_t tmem, int t, volatile int* abort_flag) {
+template <class G, bool FP16>
+__device__ void softmax_group(Smem<G>& sm, const TileArgs& a, const Work& w, uint32_t tmem, int t, volatile int* abort_flag) {
     using H = Half16<FP16>;
-    constexpr bool kSep = Geo<D>::kSepP;
+    constexpr int D = G::D;
+    constexpr bool kSep = G::kSepP;
     const int lane = threadIdx.x & 31;
     const int quarter = (threadIdx.x >> 5) & 3;  // TMEM lanes [32*quarter, 32*quarter + 32)
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_addr + col_s(t);
-    const uint32_t tO = tmem + lane_addr + Geo<D>::col_o(t);
-    const uint32_t tP = tmem + lane_addr + Geo<D>::kColP;
+    const uint32_t tO = tmem + lane_addr + G::col_o(t);
+    const uint32_t tP = tmem + lane_addr + G::kColP;
     const int n = w.n(t), n0 = w.n0, last = w.last;
     const int query = w.t0 + t * a.per_tile + row / a.p.group;
     const bool in = row < a.per_tile * a.p.group && query < w.queries;
@@ -541,7 +547,7 @@ __device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uin
                     m_used = mx;
                 }
                 l *= alpha;
-                rescale_o<D>(tO, alpha);
+                rescale_o<G>(tO, alpha);
             }
         }
         const float ref = m_used == -INFINITY ? 0.f : m_used;  // no key yet: weights 2^-inf = 0
@@ -600,16 +606,16 @@ __device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uin
     uint32_t x[D];
     if (n > 0) {
 #pragma unroll
-        for (int cc = 0; cc < Geo<D>::kChunks; ++cc) tmem_ld_x32(tO + 32u * cc, slice32(x + 32 * cc));
+        for (int cc = 0; cc < G::kChunks; ++cc) tmem_ld_x32(tO + 32u * cc, slice32(x + 32 * cc));
 #pragma unroll
-        for (int cc = 0; cc < Geo<D>::kChunks; ++cc) tmem_wait_ld_x32(slice32(x + 32 * cc));
+        for (int cc = 0; cc < G::kChunks; ++cc) tmem_wait_ld_x32(slice32(x + 32 * cc));
     }
     const bool keys = n > 0 && l != 0.f;
 #pragma unroll
     for (int i = 0; i < D; ++i) x[i] = keys ? __float_as_uint(__uint_as_float(x[i]) * inv_l) : 0u;
     if (cleared && in) {
 #pragma unroll
-        for (int cc = 0; cc < Geo<D>::kChunks; ++cc) {
+        for (int cc = 0; cc < G::kChunks; ++cc) {
             float tmp[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) tmp[i] = __uint_as_float(x[32 * cc + i]);
@@ -668,16 +674,16 @@ __device__ void softmax_group(Smem<D>& sm, const TileArgs& a, const Work& w, uin
     }
 }
 
-template <int D, bool FP16>
-__global__ void __launch_bounds__(kThreads, 1)
+template <class G, bool FP16>
+__global__ void __launch_bounds__(G::kThreads, G::kCtas)
     packed_tiles_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, const __grid_constant__ TileArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
-    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw + (((base + 1023u) & ~1023u) - base));
+    Smem<G>& sm = *reinterpret_cast<Smem<G>*>(smem_raw + (((base + 1023u) & ~1023u) - base));
     const int warp = threadIdx.x >> 5;
-    if (warp == kMmaWarp) {
-        tmem_alloc(&sm.tmem_base, kTmemCols);
+    if (warp == G::kMmaWarp) {
+        tmem_alloc(&sm.tmem_base, G::kTmemCols);
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.s_read[t], 4);
             mbar_init(&sm.pv_done[t], 1);
         }
-        for (int s = 0; s < Geo<D>::kStages; ++s) {
+        for (int s = 0; s < G::kStages; ++s) {
             mbar_init(&sm.k_full[s], 1);
             mbar_init(&sm.k_empty[s], 1);
             mbar_init(&sm.v_full[s], 1);
@@ -703,14 +709,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.nonfinite = 0;
         fence_barrier_init();
     }
-    if (warp == kProducerWarp && (threadIdx.x & 31) == 0) {
+    if (warp == G::kProducerWarp && (threadIdx.x & 31) == 0) {
         prefetch_tensor_map(&tq);
         prefetch_tensor_map(&tk);
         prefetch_tensor_map(&tv);
     }
     {
         Work mine;
-        mine.none = !find_work(a, mine);
+        mine.none = !find_work(a, G::kTiles, mine);
         if (threadIdx.x == 0) sm.work = mine;
     }
     tc_fence_before_sync();
@@ -722,64 +728,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (w.none) {
         // nothing to do
-    } else if (warp < kSoftmaxWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    } else if (warp < G::kSoftmaxWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kRegsSoftmax));
         const int t = warp >> 2;
-        if (t <= w.last) softmax_group<D, FP16>(sm, a, w, tmem, t, abort_flag);
+        if (t <= w.last) softmax_group<G, FP16>(sm, a, w, tmem, t, abort_flag);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kRegsOther));
         const bool one = (threadIdx.x & 31) == 0;
-        if (warp == kProducerWarp) {
-            if (one) producer<D>(sm, a, w, &tq, &tk, &tv, abort_flag);
-        } else if (warp == kMmaWarp) {
+        if (warp == G::kProducerWarp) {
+            if (one) producer<G>(sm, a, w, &tq, &tk, &tv, abort_flag);
+        } else if (warp == G::kMmaWarp) {
             if (one) {
-                if constexpr (Geo<D>::kSepP)
-                    qk_issuer<D, FP16>(sm, a, w, tmem, abort_flag);
+                if constexpr (G::kSepP)
+                    qk_issuer<G, FP16>(sm, a, w, tmem, abort_flag);
                 else
-                    mma_issuer<D, FP16>(sm, a, w, tmem, abort_flag);
+                    mma_issuer<G, FP16>(sm, a, w, tmem, abort_flag);
             }
-        } else if (warp == kPvWarp) {
-            if constexpr (Geo<D>::kSepP)
-                if (one) pv_issuer<D, FP16>(sm, a, w, tmem, abort_flag);
+        } else if (warp == G::kPvWarp) {
+            if constexpr (G::kSepP)
+                if (one) pv_issuer<G, FP16>(sm, a, w, tmem, abort_flag);
         } else {
-            scan_values<D, FP16>(sm, a, w, abort_flag);
+            scan_values<G, FP16>(sm, a, w, abort_flag);
         }
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == G::kMmaWarp) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, G::kTmemCols);
     }
 }
 
-template <int D, bool FP16>
+template <class G, bool FP16>
 cudaError_t run(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TileArgs& a, cudaStream_t st) {
-    constexpr size_t smem = sizeof(Smem<D>) + 1024;  // + alignment slack
-    static_assert(smem <= 232448, "shared memory per CTA");
+    constexpr size_t smem = sizeof(Smem<G>) + 1024;  // + alignment slack
+    static_assert((smem + 1024) * G::kCtas <= 233472, "shared memory of a multiprocessor");
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(packed_tiles_kernel<D, FP16>), static_cast<int>(smem), done);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(packed_tiles_kernel<G, FP16>), static_cast<int>(smem), done);
     if (e != cudaSuccess) return e;
     const int64_t grid = static_cast<int64_t>(a.pairs) * a.p.kv_heads * a.p.splits;
-    packed_tiles_kernel<D, FP16><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(tq, tk, tv, a);
+    packed_tiles_kernel<G, FP16><<<static_cast<unsigned>(grid), G::kThreads, smem, st>>>(tq, tk, tv, a);
     return cudaGetLastError();
+}
+
+template <int TILES>
+cudaError_t run(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TileArgs& a, int d, bool fp16,
+                cudaStream_t st) {
+    switch (d) {
+        case 64: return fp16 ? run<Geo<64, TILES>, true>(tq, tk, tv, a, st) : run<Geo<64, TILES>, false>(tq, tk, tv, a, st);
+        case 96: return fp16 ? run<Geo<96, TILES>, true>(tq, tk, tv, a, st) : run<Geo<96, TILES>, false>(tq, tk, tv, a, st);
+        default: return fp16 ? run<Geo<128, TILES>, true>(tq, tk, tv, a, st) : run<Geo<128, TILES>, false>(tq, tk, tv, a, st);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_packed_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& p,
-                                int d, bool fp16, int* status, uint64_t timeout_ns, cudaStream_t st) {
+                                int d, bool fp16, int tiles, int* status, uint64_t timeout_ns, cudaStream_t st) {
     TileArgs a;
     a.p = p;
-    a.pairs = static_cast<int>(packed_tile_pairs(p.total_q, p.seqs, p.group));
+    a.pairs = static_cast<int>(packed_tile_groups(p.total_q, p.seqs, p.group, tiles));
     a.per_tile = packed_queries_per_tile(p.group);
     a.status = status;
     a.timeout_ns = timeout_ns;
-    switch (d) {
-        case 64: return fp16 ? run<64, true>(tq, tk, tv, a, st) : run<64, false>(tq, tk, tv, a, st);
-        case 96: return fp16 ? run<96, true>(tq, tk, tv, a, st) : run<96, false>(tq, tk, tv, a, st);
-        default: return fp16 ? run<128, true>(tq, tk, tv, a, st) : run<128, false>(tq, tk, tv, a, st);
-    }
+    return tiles == 1 ? run<1>(tq, tk, tv, a, d, fp16, st) : run<2>(tq, tk, tv, a, d, fp16, st);
 }
 
 }  // namespace h3a

@@ -90,13 +90,13 @@ __device__ __forceinline__ int packed_limit(const PackedArgs& a, const PackedSeq
 
 // How a call is carried out (packed_plan.cu).
 struct PackedPlan {
-    bool tiles;      // 128-row tiles on tcgen05 (packed_tiles.cu), else 16 rows (packed_rows.cu)
+    int tiles;  // 128-row tiles a CTA on tcgen05 (packed_tiles.cu): 1 or 2; 0: 16 rows (packed_rows.cu)
     int splits, chunk;
 };
 PackedPlan packed_plan(const h3a_packed_desc& d);
-// Queries in a 128-row tile, and the tile pairs that hold every sequence's.
+// Queries in a 128-row tile, and the CTAs of `tiles` tiles that hold every sequence's.
 int packed_queries_per_tile(int group);
-int64_t packed_tile_pairs(int64_t total_q, int seqs, int group);
+int64_t packed_tile_groups(int64_t total_q, int seqs, int group, int tiles);
 
 // At most 16 rows (queries x group) of each sequence and kv head.
 cudaError_t launch_packed_rows(const PackedArgs& a, int d, bool fp16, cudaStream_t st);
@@ -104,7 +104,7 @@ cudaError_t launch_packed_rows(const PackedArgs& a, int d, bool fp16, cudaStream
 // packed_queries_per_tile} box, k and v as {d, kv_heads, total_k} with {32, 1,
 // 128} boxes, 64-byte swizzle.
 cudaError_t launch_packed_tiles(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& p,
-                                int d, bool fp16, int* status, uint64_t timeout_ns, cudaStream_t st);
+                                int d, bool fp16, int tiles, int* status, uint64_t timeout_ns, cudaStream_t st);
 cudaError_t launch_packed_combine(const PackedArgs& a, int d, bool fp16, cudaStream_t st);
 
 }  // namespace h3a
