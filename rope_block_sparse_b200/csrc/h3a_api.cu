@@ -243,7 +243,9 @@ h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, size_t* rows
     *plan = packed_plan(*d);
     const int group = d->heads / d->kv_heads;
     const double columns = plan->tiles ? static_cast<double>(packed_tile_groups(d->total_q, d->seqs, group, plan->tiles)) : d->seqs;
-    const double grid = columns * d->kv_heads * plan->splits;
+    // the tile kernel's grid has the kv heads as its second dimension
+    const double grid = plan->tiles ? (d->kv_heads > 65535 ? static_cast<double>(lim) : columns)
+                                    : columns * d->kv_heads * plan->splits;
     const double rows = static_cast<double>(d->total_q) * d->heads;
     if (grid >= static_cast<double>(lim) || rows >= 4.0 * static_cast<double>(lim)) return H3A_ERR_UNSUPPORTED;
     *rows_bytes = *bytes = 0;

@@ -6,7 +6,7 @@
 #include "prompt_internal.h"
 
 #ifndef ONE_TILE_KEYS
-#define ONE_TILE_KEYS 1024
+#define ONE_TILE_KEYS -1
 #endif
 namespace h3a {
 
@@ -34,7 +34,12 @@ PackedPlan packed_plan(const h3a_packed_desc& d) {
     // Up to 16 rows (queries x heads of a group) fit one mma.m16n8k16 tile of
     // the row kernel, which then reads the keys once; more go to the 128-row
     // tiles of the tcgen05 kernel.
-    p.tiles = max_q * group <= 16 ? 0 : max_k <= ONE_TILE_KEYS ? 1 : 2;
+    // One tile a CTA for short sequences, two for long ones (us, one against two;
+    // 16 prompts): 32/8 heads x 128 up to 300 keys 21.8 / 24.1, 700 51.6 / 53.1, 1,000
+    // 77.9 / 76.8; 28/4 x 96 up to 700 40.3 / 41.1, 1,000 60.5 / 59.2; 16 x 64 up to
+    // 2,000 87.9 / 98.3, but one prompt of 16,000 792 / 771.
+    const int64_t one_tile = ONE_TILE_KEYS >= 0 ? ONE_TILE_KEYS : d.head_dim == 64 ? 4096 : 768;
+    p.tiles = max_q * group <= 16 ? 0 : max_k <= one_tile ? 1 : 2;
     int64_t splits, chunk;
     if (p.tiles) {
         // a part for every multiprocessor without work, each of at least 512

@@ -156,19 +156,17 @@ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
 // memory is what this takes.
 __device__ __forceinline__ bool find_work(const TileArgs& a, int tiles, Work& w) {
     const int lane = threadIdx.x & 31;
-    uint32_t at = blockIdx.x;
-    const int pair = a.pairs - 1 - static_cast<int>(at % a.pairs);
-    at /= a.pairs;
-    w.kvh = at % a.p.kv_heads;
-    w.split = at / a.p.kv_heads;
-    const int span = tiles * a.per_tile;
+    const int pair = a.pairs - 1 - static_cast<int>(blockIdx.x);
+    w.kvh = blockIdx.y;
+    w.split = blockIdx.z;
+    const uint32_t span = tiles * a.per_tile;
     int lo = 0, hi = a.p.seqs;  // the last sequence in [lo, hi) whose pairs start at or before this one
     PackedSeq mine;
     int first;
     for (;;) {
         const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
         mine = packed_seq(a.p, min(probe, a.p.seqs - 1));
-        first = static_cast<int>(mine.q0 / span) + probe;
+        first = static_cast<int>(static_cast<uint32_t>(mine.q0) / span) + probe;
         // lane 0 stands for lo itself
         const uint32_t yes = __ballot_sync(0xffffffffu, lane == 0 || (probe < hi && first <= pair));
         const int winner = 31 - __clz(yes);
@@ -183,7 +181,7 @@ __device__ __forceinline__ bool find_work(const TileArgs& a, int tiles, Work& w)
         lo += winner * step;
         hi = min(hi, lo + step);
     }
-    const int64_t t0 = static_cast<int64_t>(pair - first) * span;
+    const int64_t t0 = static_cast<int64_t>(pair - first) * static_cast<int>(span);
     w.queries = static_cast<int>(min(static_cast<int64_t>(w.s.lq), a.p.max_q));
     if (t0 < 0 || t0 >= w.queries) return false;
     w.t0 = static_cast<int>(t0);
@@ -461,12 +459,17 @@ __device__ void softmax_group(Smem<G>& sm, const TileArgs& a, const Work& w, uin
     const uint32_t tO = tmem + lane_addr + G::col_o(t);
     const uint32_t tP = tmem + lane_addr + G::kColP;
     const int n = w.n(t), n0 = w.n0, last = w.last;
-    const int query = w.t0 + t * a.per_tile + row / a.p.group;
-    const bool in = row < a.per_tile * a.p.group && query < w.queries;
-    // rows that are no query's see what the tile sees (and are not written), so
-    // that they do not cost their warp the comparisons
-    const int limit = in ? min(packed_limit(a.p, w.s, query), w.end(t)) : w.end(t);
-    int valid = max(limit - w.begin, 0);  // keys of the step and behind that the row attends
+    // the row's query in the sequence, -1 if it has none
+    auto query_of_row = [&]() {
+        const int query = w.t0 + t * a.per_tile + row / a.p.group;
+        return row < a.per_tile * a.p.group && query < w.queries ? query : -1;
+    };
+    // Keys of the tile that the row attends.  Rows that are no query's see what the
+    // tile sees (and are not written), so that they do not cost their warp the
+    // comparisons.
+    auto limit_of = [&](int query) { return query >= 0 ? min(packed_limit(a.p, w.s, query), w.end(t)) : w.end(t); };
+    const bool in = G::kTiles == 1 && query_of_row() >= 0;
+    int valid = max(limit_of(query_of_row()) - w.begin, 0);  // keys of the step and behind that the row attends
     // Separate P: before this tile writes the shared P buffer at step j, the PV
     // that last read it must have completed -- the other tile's of step j - 1
     // (tile 0) or j (tile 1) as long as that tile runs, else this tile's own of
@@ -491,54 +494,20 @@ __device__ void softmax_group(Smem<G>& sm, const TileArgs& a, const Work& w, uin
             break;
         }
         tc_fence_after_sync();
-        const bool partly = __any_sync(0xffffffffu, valid < 128);
-        uint32_t x[128];
-        float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int q = 0; q < 2; ++q) tmem_ld_x32(tS + 32u * q, slice32(x + 32 * q));
-#pragma unroll
-        for (int q = 0; q < 2; ++q) tmem_wait_ld_x32(slice32(x + 32 * q));
-#pragma unroll
-        for (int q = 2; q < 4; ++q) tmem_ld_x32(tS + 32u * q, slice32(x + 32 * q));
-        if (partly) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (i >= valid) x[i] = __float_as_uint(-INFINITY);
-        }
-        // first half's max while the second half loads
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            pm[i & 3] = max3(pm[i & 3], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-#pragma unroll
-        for (int q = 2; q < 4; ++q) tmem_wait_ld_x32(slice32(x + 32 * q));
-        if constexpr (kSep) {
-            // S_t is in registers: release it for QK_t(j+1)
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_read[t]);
-        }
+        // Moves the reference to the step's maximum mx where it must (and O with
+        // it): at the first step, and when a row's maximum grew by 2^8 or it had no
+        // key before.  O_t must be stable then: with P over S the commit behind
+        // s_full covers PV_t(j-1); with a separate P buffer, its wait does.
         bool p_free = false;
-        if (partly) {
-#pragma unroll
-            for (int i = 64; i < 128; ++i)
-                if (i >= valid) x[i] = __float_as_uint(-INFINITY);
-        }
-#pragma unroll
-        for (int i = 32; i < 64; ++i)
-            pm[i & 3] = max3(pm[i & 3], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-        const float mx = c * fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-        if (j == 0) {
-            m_used = mx;  // the first step fixes the reference
-        } else {
-            const bool need = mx - m_used > 8.0f;  // also a row's first key, from a reference of -inf
+        auto refer = [&](float mx) -> bool {
+            if (j == 0) {
+                m_used = mx;
+                return true;
+            }
+            const bool need = mx - m_used > 8.0f;
             if (__any_sync(0xffffffffu, need)) {
-                // O_t must be stable: with P over S the commit behind s_full
-                // covers PV_t(j-1); with a separate P buffer, its wait does
                 if constexpr (kSep) {
-                    if (!wait_p_buffer(j)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!wait_p_buffer(j)) return false;
                     p_free = true;
                 }
                 float alpha = 1.0f;
@@ -549,32 +518,118 @@ __device__ void softmax_group(Smem<G>& sm, const TileArgs& a, const Work& w, uin
                 l *= alpha;
                 rescale_o<G>(tO, alpha);
             }
-        }
-        const float ref = m_used == -INFINITY ? 0.f : m_used;  // no key yet: weights 2^-inf = 0
-        const uint64_t c2 = f2(c, c), nm2 = f2(-ref, -ref);
-        uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            float a0, a1;
-            f2_split(f2_fma(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, nm2), a0, a1);
-            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-            acc[i & 1] = f2_add(acc[i & 1], f2(p0, p1));
-            x[i] = H::pack(p0, p1);
-            if constexpr (!kSep)
-                if ((i & 15) == 15) tmem_st_x16(tS + (i - 15), slice16(x + (i - 15)));
-        }
-        if constexpr (kSep) {
-            if (!p_free && !wait_p_buffer(j)) {
-                ok = false;
-                break;
+            return true;
+        };
+        auto s_is_read = [&]() {
+            if constexpr (kSep) {
+                // S_t is in registers: release it for QK_t(j+1)
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.s_read[t]);
             }
-            tmem_st_x32(tP, slice32(x));
-            tmem_st_x32(tP + 32u, slice32(x + 32));
+        };
+        uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+        const uint64_t c2 = f2(c, c);
+        const bool partly = __any_sync(0xffffffffu, valid < 128);  // some row does not attend some key
+        if (G::kTiles == 2 || !partly) {
+            // the row in registers, all of it unrolled
+            uint32_t x[128];
+            float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) tmem_ld_x32(tS + 32u * q, slice32(x + 32 * q));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) tmem_wait_ld_x32(slice32(x + 32 * q));
+#pragma unroll
+            for (int q = 2; q < 4; ++q) tmem_ld_x32(tS + 32u * q, slice32(x + 32 * q));
+            if (G::kTiles == 2 && partly) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    if (i >= valid) x[i] = __float_as_uint(-INFINITY);
+            }
+            // first half's max while the second half loads
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                pm[i & 3] = max3(pm[i & 3], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+#pragma unroll
+            for (int q = 2; q < 4; ++q) tmem_wait_ld_x32(slice32(x + 32 * q));
+            s_is_read();
+            if (G::kTiles == 2 && partly) {
+#pragma unroll
+                for (int i = 64; i < 128; ++i)
+                    if (i >= valid) x[i] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int i = 32; i < 64; ++i)
+                pm[i & 3] = max3(pm[i & 3], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            if (!(ok = refer(c * fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]))))) break;
+            const float ref = m_used == -INFINITY ? 0.f : m_used;  // no key yet: weights 2^-inf = 0
+            const uint64_t nm2 = f2(-ref, -ref);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+                float a0, a1;
+                f2_split(f2_fma(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, nm2), a0, a1);
+                const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+                acc[i & 1] = f2_add(acc[i & 1], f2(p0, p1));
+                x[i] = H::pack(p0, p1);
+                if constexpr (!kSep)
+                    if ((i & 15) == 15) tmem_st_x16(tS + (i - 15), slice16(x + (i - 15)));
+            }
+            if constexpr (kSep) {
+                if (!p_free && !(ok = wait_p_buffer(j))) break;
+                tmem_st_x32(tP, slice32(x));
+                tmem_st_x32(tP + 32u, slice32(x + 32));
+            }
+        } else {
+            // One tile, where the keys end or the diagonal passes: 32 columns at a
+            // time, as far as any row of the warp attends them, S read once for the
+            // maximum and once for the weights.  Not unrolled: a short sequence
+            // runs through this once or twice, and fetching the instructions is
+            // then most of what it costs.  (16 prompts of up to 1,000, 16 heads x
+            // 64: 39.0 us against 45.6 by the row in registers.  With two tiles,
+            // which take turns at the tensor core, the longer step costs more than
+            // it saves: 52.2 us against 46.9.)
+            const int top = __reduce_max_sync(0xffffffffu, in ? min(max(valid, 0), 128) : 0);
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int k = 0; k < top; k += 32) {
+                uint32_t x[32];
+                tmem_ld_x32(tS + k, x);
+                tmem_wait_ld_x32(x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) mx = fmaxf(mx, k + i < valid ? __uint_as_float(x[i]) : -INFINITY);
+            }
+            if (!(ok = refer(c * mx))) break;
+            const float ref = m_used == -INFINITY ? 0.f : m_used;
+            const uint64_t nm2 = f2(-ref, -ref);
+            if constexpr (kSep)
+                if (!p_free && !(ok = wait_p_buffer(j))) break;
+#pragma unroll 1
+            for (int k = 0; k < 128; k += 32) {
+                uint32_t x[32];
+                if (k < top) {
+                    tmem_ld_x32(tS + k, x);
+                    tmem_wait_ld_x32(x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float a0, a1;
+                        f2_split(f2_fma(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, nm2), a0, a1);
+                        const float p0 = k + 2 * i < valid ? ex2_approx(a0) : 0.f, p1 = k + 2 * i + 1 < valid ? ex2_approx(a1) : 0.f;
+                        acc[i & 1] = f2_add(acc[i & 1], f2(p0, p1));
+                        x[i] = H::pack(p0, p1);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = 0;
+                }
+                tmem_st_x16((kSep ? tP : tS) + k / 2, slice16(x));  // P over S: behind what was read last
+            }
+            s_is_read();
         }
         float s0, s1, s2, s3;
         f2_split(acc[0], s0, s1);
         f2_split(acc[1], s2, s3);
         l += (s0 + s1) + (s2 + s3);
+        // one arrival per warp: every lane's TMEM stores are complete and fenced
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -585,7 +640,10 @@ __device__ void softmax_group(Smem<G>& sm, const TileArgs& a, const Work& w, uin
         raise_timeout(a, abort_flag);
         return;
     }
-    if (n == 0 && w.split > 0) return;
+    // what the rows' end needs is worked out again: it does not sit in registers during the loop
+    const int query = query_of_row();
+    const bool there = query >= 0;
+    if ((n == 0 && w.split > 0) || !__any_sync(0xffffffffu, there)) return;
     tc_fence_after_sync();
     const bool cleared = *reinterpret_cast<volatile int*>(&sm.nonfinite) != 0;
     const float inv_l = l == 0.f ? 0.f : 1.0f / l;
@@ -594,79 +652,64 @@ __device__ void softmax_group(Smem<G>& sm, const TileArgs& a, const Work& w, uin
     const int64_t tok = w.s.q0 + query, qh = tok * a.p.heads + head;
     const bool split = a.p.splits > 1;
     // A warp's 32 rows go out through the Q tile's shared memory (no MMA reads
-    // it any more) as whole rows: a thread's own row would be written 16 bytes
-    // here and 16 there.  16-byte chunks are swizzled by the row so that neither
-    // side collides.
+    // it any more), 64 or 128 bytes of each at a time, so that a warp writes whole
+    // pieces of rows: a thread's own row would be written 16 bytes here and 16
+    // there.  16-byte pieces are swizzled by the row so that neither side collides.
     const int64_t rows = a.p.total_q * a.p.heads;
     int64_t* places = sm.place[t * 4 + quarter];
-    places[lane] = !in ? -1 : split ? (w.split * rows + qh) * D : tok * a.p.on + head * a.p.oh;
+    places[lane] = !there ? -1 : split ? (w.split * rows + qh) * D : tok * a.p.on + head * a.p.oh;
     uint4* stage = reinterpret_cast<uint4*>(sm.q[t]) + quarter * 32 * (D / 8);
-    constexpr int kPieces = D / 8;  // 16-byte chunks of a row of the element type
-    constexpr int kSwap = kPieces % 8 ? 3 : 7;
-    uint32_t x[D];
-    if (n > 0) {
-#pragma unroll
-        for (int cc = 0; cc < G::kChunks; ++cc) tmem_ld_x32(tO + 32u * cc, slice32(x + 32 * cc));
-#pragma unroll
-        for (int cc = 0; cc < G::kChunks; ++cc) tmem_wait_ld_x32(slice32(x + 32 * cc));
-    }
+    __syncwarp();
     const bool keys = n > 0 && l != 0.f;
+#pragma unroll 1
+    for (int cc = 0; cc < G::kChunks; ++cc) {
+        uint32_t x[32];
+        if (n > 0) {
+            tmem_ld_x32(tO + 32u * cc, x);
+            tmem_wait_ld_x32(x);
+        }
 #pragma unroll
-    for (int i = 0; i < D; ++i) x[i] = keys ? __float_as_uint(__uint_as_float(x[i]) * inv_l) : 0u;
-    if (cleared && in) {
-#pragma unroll
-        for (int cc = 0; cc < G::kChunks; ++cc) {
+        for (int i = 0; i < 32; ++i) x[i] = keys ? __float_as_uint(__uint_as_float(x[i]) * inv_l) : 0u;
+        if (cleared && there) {
             float tmp[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) tmp[i] = __uint_as_float(x[32 * cc + i]);
+            for (int i = 0; i < 32; ++i) tmp[i] = __uint_as_float(x[i]);
             add_nonfinite<FP16>(tmp, static_cast<const uint16_t*>(a.p.v) + w.s.k0 * a.p.vn + w.kvh * a.p.vh + 32 * cc, a.p.vn,
-                                w.begin + 128 * w.clean, limit);
+                                w.begin + 128 * w.clean, limit_of(query));
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[32 * cc + i] = __float_as_uint(tmp[i]);
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(tmp[i]);
         }
-    }
-    // rows [lane / per, + 32 / per, ...) of the staged chunks, `per` lanes a row
-    auto out = [&](auto* base, int pieces, int swap, int first_channel) {
+        if (split) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint4 v[kPieces / 2];
-            int64_t at[kPieces / 2];
-#pragma unroll
-            for (int i = 0; i < kPieces / 2; ++i) {
-                const int piece = (half * (kPieces / 2) + i) * 32 + lane, r = piece / pieces, c = piece % pieces;
-                v[i] = stage[r * pieces + (c ^ (r & swap))];
-                at[i] = places[r];
-                if (at[i] >= 0) at[i] += first_channel + c * (16 / static_cast<int>(sizeof(*base)));
-            }
-#pragma unroll
-            for (int i = 0; i < kPieces / 2; ++i)
-                if (at[i] >= 0) *reinterpret_cast<uint4*>(base + at[i]) = v[i];
-        }
-    };
-    if (split) {
-        // fp32 rows, half of the channels at a time
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int c = h * (D / 2) + 4 * i;
-                stage[lane * kPieces + (i ^ (lane & kSwap))] = make_uint4(x[c], x[c + 1], x[c + 2], x[c + 3]);
-            }
+            for (int i = 0; i < 8; ++i)
+                stage[lane * 8 + (i ^ (lane & 7))] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
             __syncwarp();
-            out(a.p.part_o, kPieces, kSwap, h * (D / 2));
-            __syncwarp();
-        }
-    } else {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            auto f = [&](int e) { return __uint_as_float(x[8 * i + e]); };
-            stage[lane * kPieces + (i ^ (lane & kSwap))] =
-                make_uint4(H::pack(f(0), f(1)), H::pack(f(2), f(3)), H::pack(f(4), f(5)), H::pack(f(6), f(7)));
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + lane / 8, piece = lane & 7;
+                const uint4 v = stage[r * 8 + (piece ^ (r & 7))];
+                const int64_t at = places[r];
+                if (at >= 0) reinterpret_cast<uint4*>(a.p.part_o + at + 32 * cc)[piece] = v;
+            }
+        } else {
+            uint32_t h[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) h[i] = H::pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 8 + lane / 4, piece = lane & 3;
+                const uint4 v = stage[r * 4 + (piece ^ ((r >> 1) & 3))];
+                const int64_t at = places[r];
+                if (at >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.p.o) + at + 32 * cc)[piece] = v;
+            }
         }
         __syncwarp();
-        out(static_cast<uint16_t*>(a.p.o), kPieces, kSwap, 0);
     }
-    if (in) {
+    if (there) {
         if (split)
             a.p.part_lse[w.split * rows + qh] = lse2;
         else if (a.p.lse)
@@ -766,8 +809,8 @@ cudaError_t run(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap&
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(packed_tiles_kernel<G, FP16>), static_cast<int>(smem), done);
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(a.pairs) * a.p.kv_heads * a.p.splits;
-    packed_tiles_kernel<G, FP16><<<static_cast<unsigned>(grid), G::kThreads, smem, st>>>(tq, tk, tv, a);
+    const dim3 grid(a.pairs, a.p.kv_heads, a.p.splits);
+    packed_tiles_kernel<G, FP16><<<grid, G::kThreads, smem, st>>>(tq, tk, tv, a);
     return cudaGetLastError();
 }
 
