@@ -1,4 +1,5 @@
-"""Build libh3a.so in-tree for sm_100a with nvcc.
+"""Build libh3a.so in-tree for sm_100a with nvcc, and _binding.so (csrc/binding.cpp)
+against the installed torch with g++.
 
     python -m rope_block_sparse_b200.build [--force] [--verbose]
 
@@ -22,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libh3a.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["h3a_api.cu", "prologue.cu", "router.cu", "attention.cu", "selftest.cu", "route_noalloc.cu", "dit_ops.cu",
            "rope.cu", "rmsnorm.cu", "packed_plan.cu", "packed_tiles.cu", "packed_rows.cu", "packed_combine.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -43,10 +45,26 @@ def _inputs() -> list:
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _binding_cmd(out: str) -> list:
+    """g++ of the torch binding; it finds libh3a.so beside itself."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    includes = [os.path.join(root, "include"), sysconfig.get_paths()["include"], cuda]
+    libs = os.path.join(root, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", INCLUDE, *[x for i in includes for x in ("-isystem", i)], os.path.join(CSRC, "binding.cpp"), "-o", out,
+            "-L", libs, "-L", PKG, "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}", "-l:libh3a.so", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -71,9 +89,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if failed:
         raise RuntimeError(f"nvcc failed on {failed}")
     tmp = LIB + f".tmp{os.getpid()}"
-    link = [nvcc, *ARCH, "-shared", "-o", tmp, *[o for _, o, _, _ in procs], "-cudart", "static"]
+    link = [nvcc, *ARCH, "-shared", "-o", tmp, "-Xlinker", "-soname=libh3a.so", *[o for _, o, _, _ in procs], "-cudart", "static"]
     subprocess.check_call(link)
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    subprocess.check_call(_binding_cmd(tmp))
+    os.replace(tmp, BINDING)
     return LIB
 
 

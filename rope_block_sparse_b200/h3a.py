@@ -421,56 +421,14 @@ _SCALES = {None: 0, "row": 1, "group": 2}  # h3a_scales
 SCALE_GROUP = 128  # H3A_SCALE_GROUP
 
 
-def _launch(fn: str, call, index: int, *args):
-    """Call an entry point on the current stream of device `index`, whichever device is the current one."""
-    if index == torch._C._cuda_getDevice():
-        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status:
-        _check(fn, status)
+@functools.cache
+def _binding():
+    """The compiled binding of the prompt side's calls (csrc/binding.cpp; raises if it was not built)."""
+    load()
+    from . import _binding as module
 
-
-# A single-token step's kernels take a few microseconds, so what follows keeps the host's part short:
-# what depends on shapes, strides and types alone (checks, descriptors) is worked out once for each
-# combination of them and looked up after that (fresh outputs follow from the inputs).  Nothing of a tensor's contents or address is kept.
-_layouts: dict = {}
-
-
-def _layout(key, got):
-    if len(_layouts) >= 4096:
-        _layouts.clear()
-    _layouts[key] = got
-    return got
-
-
-def _sig(t: torch.Tensor | None):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
-
-
-def _empty(t: torch.Tensor) -> torch.Tensor:
-    """A contiguous tensor of t's shape and type."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
-
-
-def _check_rows(name: str, t: torch.Tensor, dims: int, like: torch.Tensor | None = None) -> int:
-    """The h3a_dtype of a bf16 / fp16 CUDA tensor whose last dimension is contiguous."""
-    dtype = _DTYPES.get(t.dtype)
-    if dtype is None:
-        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device (libh3a has no CPU path)")
-    if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must have the element type and device of the first tensor")
-    return dtype
-
-
-def _check_index(name: str, t: torch.Tensor, n: int, device: torch.device):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on {device}")
+    module.set_error(H3AError)
+    return module
 
 
 def rope_plan(rotary_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
@@ -509,43 +467,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, plan:
     kv_heads, head_dim] (or None), any strides with head_dim contiguous (slices of a fused QKV buffer).
     positions: int32 [tokens].  inverse rotates back.  Returns (q_out, k_out); inplace=True overwrites
     q and k, out=(q_out, k_out) writes into given tensors."""
-    if inplace:
-        q_out, k_out, key = q, k, ("rope in place", _sig(q), _sig(k), _sig(positions))
-    elif out is not None:
-        q_out, k_out = out
-        key = ("rope out", _sig(q), _sig(k), _sig(q_out), _sig(k_out), _sig(positions))
-    else:
-        q_out, k_out = _empty(q), (None if k is None else _empty(k))
-        key = ("rope", _sig(q), _sig(k), _sig(positions))
-    lay = _layouts.get(key) or _layout(key, _rope_layout(q, k, q_out, k_out, positions))
-    call, index, dtype, tokens, dq, dk = lay
-    if k is None:
-        _launch("h3a_rope", call, index, q.data_ptr(), q_out.data_ptr(), dq, None, None, None, dtype,
-                positions.data_ptr(), tokens, plan, inverse)
-    else:
-        _launch("h3a_rope", call, index, q.data_ptr(), q_out.data_ptr(), dq, k.data_ptr(), k_out.data_ptr(), dk, dtype,
-                positions.data_ptr(), tokens, plan, inverse)
-    return q_out, k_out
-
-
-def _rope_layout(q, k, q_out, k_out, positions):
-    dtype = _check_rows("q", q, 3)
-    tokens = q.shape[0]
-    _check_index("positions", positions, tokens, q.device)
-    if (k is None) != (k_out is None):
-        raise ValueError("out must hold a tensor for q, and for k where k is given")
-    if k is not None:
-        _check_rows("k", k, 3, q)
-        if k.shape[0] != tokens or k.shape[2] != q.shape[2]:
-            raise ValueError("q and k must have the same tokens and head_dim")
-
-    def desc(x, y):
-        _check_rows("out", y, 3, q)
-        if y.shape != x.shape:
-            raise ValueError("out must have the shapes of q and k")
-        return HeadsDesc(x.shape[1], x.shape[2], x.stride(0), x.stride(1), y.stride(0), y.stride(1))
-
-    return load().h3a_rope, q.device.index, dtype, tokens, desc(q, q_out), (None if k is None else desc(k, k_out))
+    q_out, k_out = (q, k) if inplace else (None, None) if out is None else out
+    return _binding().rope(q, k, positions, plan, inverse, q_out, k_out)
 
 
 def residual_rmsnorm(x: torch.Tensor, f: torch.Tensor | None, gamma: torch.Tensor, eps: float = 1e-6,
@@ -555,64 +478,17 @@ def residual_rmsnorm(x: torch.Tensor, f: torch.Tensor | None, gamma: torch.Tenso
     "group" (128 channels): y in float8_e4m3fn with fp32 scales [rows] or [rows, ceil(C / 128)], so that
     y * scale stands for the normalised row.  Returns (h or None, y, scales or None); out=(h, y, scales)
     writes into given tensors (h may be x or f)."""
-    if out is not None:
-        h, y, s = out
-        if f is None:
-            h = None
-        if scales is None:
-            s = None
-        key = ("rmsnorm out", scales, _sig(x), _sig(f), _sig(gamma), _sig(h), _sig(y), _sig(s))
-    else:
-        h = None if f is None else _empty(x)
-        if scales is None:
-            y, s = _empty(x), None
-        else:
-            y = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
-            rows, width = x.shape
-            s = gamma.new_empty(rows if scales == "row" else (rows, -(-width // SCALE_GROUP)))
-        key = ("rmsnorm", scales, _sig(x), _sig(f), _sig(gamma))
-    lay = _layouts.get(key) or _layout(key, _rmsnorm_layout(x, f, gamma, scales, h, y, s))
-    call, index, xs, fs, rows, width, dtype, code, hs, ys = lay
-    _launch("h3a_residual_rmsnorm", call, index, x.data_ptr(), xs, None if f is None else f.data_ptr(), fs,
-            gamma.data_ptr(), rows, width, dtype, eps, code, None if h is None else h.data_ptr(), hs, y.data_ptr(), ys,
-            None if s is None else s.data_ptr())
-    return h, y, s
-
-
-def _rmsnorm_layout(x, f, gamma, scales, h, y, s):
-    dtype = _check_rows("x", x, 2)
-    rows, width = x.shape
-    if scales not in _SCALES:
+    code = _SCALES.get(scales)
+    if code is None:
         raise ValueError(f'scales must be None, "row" or "group", got {scales!r}')
-    for name, t in (("f", f), ("h", h)):
-        if f is None:
-            continue
-        if t is None:
-            raise ValueError("a residual needs an h output")
-        _check_rows(name, t, 2, x)
-        if t.shape != x.shape:
-            raise ValueError(f"{name} must match x")
-    if gamma.dtype != torch.float32 or gamma.shape != (width,) or not gamma.is_contiguous() or gamma.device != x.device:
-        raise ValueError("gamma must be a contiguous fp32 [C] tensor on x's device")
-    y_type = x.dtype if scales is None else torch.float8_e4m3fn
-    if y.dtype != y_type or y.shape != x.shape or (y.stride(1) != 1 and width > 1) or y.device != x.device:
-        raise ValueError(f"y must be a {y_type} tensor of x's shape, rows contiguous")
-    if scales is not None:
-        shape = (rows,) if scales == "row" else (rows, -(-width // SCALE_GROUP))
-        if s is None or s.dtype != torch.float32 or s.shape != shape or not s.is_contiguous() or s.device != x.device:
-            raise ValueError(f"scales must be a contiguous fp32 {shape} tensor")
-
-    def step(t):  # a single row is not stepped: any stride
-        return t.stride(0) if t is not None and rows > 1 else width
-
-    return (load().h3a_residual_rmsnorm, x.device.index, step(x), step(f), rows, width, dtype, _SCALES[scales], step(h),
-            step(y))
+    h, y, s = (None, None, None) if out is None else out
+    return _binding().residual_rmsnorm(x, f, gamma, eps, code, h, y, s)
 
 
 def packed_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, seqs: int, max_q: int, max_k: int) -> int:
     """Bytes of workspace packed_attention() needs for these shapes (0: none)."""
     n = ctypes.c_size_t(0)
-    d = PackedDesc(_check_rows("q", q, 3), seqs, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], max_q, max_k,
+    d = PackedDesc(_DTYPES[q.dtype], seqs, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], max_q, max_k,
                    *q.stride()[:2], *k.stride()[:2], *k.stride()[:2], *q.stride()[:2], 1, 0.0)
     _check("h3a_packed_attention_workspace_size", load().h3a_packed_attention_workspace_size(d, n))
     return n.value
@@ -630,51 +506,8 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts_q
     longest sequence's queries and keys (host numbers).  A query without keys gets zeros.  Returns o, or
     (o, lse) with the natural log-sum-exps, fp32 [total_q, heads]; rows outside every sequence are left as
     they were (in `out`) or undefined."""
-    if out is None:
-        out = _empty(q)
-        key = ("packed", _sig(q), _sig(k), _sig(v), _sig(starts_q), _sig(starts_k), _sig(lengths_k))
-    else:
-        key = ("packed out", _sig(q), _sig(k), _sig(v), _sig(starts_q), _sig(starts_k), _sig(lengths_k), _sig(out))
-    lay = _layouts.get(key) or _layout(key, _packed_layout(q, k, v, out, starts_q, starts_k, lengths_k))
-    call, size_of, index, head, strides = lay
-    d = PackedDesc(*head, max_q, max_k, *strides, causal, scale)
-    if workspace is None:
-        n = ctypes.c_size_t(0)
-        status = size_of(d, n)
-        if status:
-            _check("h3a_packed_attention", status)
-        room = n.value
-        if room:
-            workspace = torch.empty(room, dtype=torch.uint8, device=q.device)
-    else:
-        if not workspace.is_contiguous() or workspace.device != q.device:
-            raise ValueError("workspace must be a contiguous tensor on q's device")
-        room = workspace.numel() * workspace.element_size()
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
-    _launch("h3a_packed_attention", call, index, q.data_ptr(), k.data_ptr(), v.data_ptr(), d, starts_q.data_ptr(),
-            starts_k.data_ptr(), None if lengths_k is None else lengths_k.data_ptr(), out.data_ptr(),
-            None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), room)
-    return (out, lse) if return_lse else out
-
-
-def _packed_layout(q, k, v, out, starts_q, starts_k, lengths_k):
-    dtype = _check_rows("q", q, 3)
-    device = q.device
-    for name, t in (("k", k), ("v", v), ("out", out)):
-        _check_rows(name, t, 3, q)
-    if k.shape != v.shape or k.shape[2] != q.shape[2]:
-        raise ValueError("k and v must have one shape, and q's head_dim")
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    seqs = starts_q.shape[0] - 1 if starts_q.dim() == 1 else 0
-    _check_index("starts_q", starts_q, seqs + 1, device)
-    _check_index("starts_k", starts_k, seqs + 1, device)
-    if lengths_k is not None:
-        _check_index("lengths_k", lengths_k, seqs, device)
-    lib = load()
-    return (lib.h3a_packed_attention, lib.h3a_packed_attention_workspace_size, device.index,
-            (dtype, seqs, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0]),
-            (*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2]))
+    return _binding().packed_attention(q, k, v, starts_q, starts_k, max_q, max_k, lengths_k, causal, scale, return_lse,
+                                       workspace, out)
 
 
 def last_device_error() -> int:
