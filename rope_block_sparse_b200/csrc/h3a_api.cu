@@ -247,7 +247,7 @@ h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, size_t* rows
     const double grid = plan->tiles ? (d->kv_heads > 65535 ? static_cast<double>(lim) : columns)
                                     : columns * d->kv_heads * plan->splits;
     const double rows = static_cast<double>(d->total_q) * d->heads;
-    if (grid >= static_cast<double>(lim) || rows >= 4.0 * static_cast<double>(lim)) return H3A_ERR_UNSUPPORTED;
+    if (grid >= static_cast<double>(lim) || rows >= static_cast<double>(lim)) return H3A_ERR_UNSUPPORTED;
     *rows_bytes = *bytes = 0;
     if (plan->splits > 1) {
         const size_t parts = static_cast<size_t>(plan->splits) * static_cast<size_t>(d->total_q) * d->heads;

@@ -2,11 +2,15 @@
 // many parts a sequence's keys are cut.  Host only; goes by the descriptor's
 // sizes, so the workspace size follows from the descriptor alone.
 #include <algorithm>
+#include <cmath>
 
 #include "prompt_internal.h"
 
 #ifndef ONE_TILE_KEYS
 #define ONE_TILE_KEYS -1
+#endif
+#ifndef JOINUS
+#define JOINUS 3.0
 #endif
 namespace h3a {
 
@@ -26,6 +30,28 @@ int packed_queries_per_tile(int group) { return 128 / group; }
 int64_t packed_tile_groups(int64_t total_q, int seqs, int group, int tiles) {
     return total_q / (tiles * packed_queries_per_tile(group)) + seqs;
 }
+
+namespace {
+
+// Parts for the row kernel: what is estimated to end first.  Two CTAs a
+// multiprocessor take 64 keys in about 0.4 us each, a CTA's beginning and end
+// about 2 us; joining the parts is a second launch.
+int64_t row_splits(const h3a_packed_desc& d, int64_t max_k) {
+    const double base = static_cast<double>(d.seqs) * d.kv_heads, units = static_cast<double>((max_k + 63) / 64);
+    int64_t best = 1;
+    double least = 0;
+    for (int64_t s = 1; s <= 256 && s <= units; s += s < 16 ? 1 : s / 8) {
+        const double waves = std::max(1.0, base * s / (2 * kSms));
+        const double us = waves * (std::ceil(units / s) * 0.4 + 2.0) + (s > 1 ? JOINUS + 0.03 * s : 0.0);
+        if (s == 1 || us < 0.9 * least) {
+            best = s;
+            least = us;
+        }
+    }
+    return best;
+}
+
+}  // namespace
 
 PackedPlan packed_plan(const h3a_packed_desc& d) {
     PackedPlan p{};
@@ -50,17 +76,8 @@ PackedPlan packed_plan(const h3a_packed_desc& d) {
         splits = std::max<int64_t>(1, std::min<int64_t>(splits, 64));
         chunk = ((max_k + splits - 1) / splits + 127) / 128 * 128;
     } else {
-        // Keys of a part: small enough that the parts fill the GPU about twice
-        // over and long sequences do not outlast the rest, at least 128 and at
-        // most 1,024.
-        const int64_t base = static_cast<int64_t>(d.seqs) * d.kv_heads;
-        chunk = max_k * base / (4 * kSms) / 64 * 64;
-        chunk = std::max<int64_t>(128, std::min<int64_t>(chunk, 1024));
-        splits = (max_k + chunk - 1) / chunk;
-        if (splits > 256) {
-            splits = 256;
-            chunk = ((max_k + 255) / 256 + 63) / 64 * 64;
-        }
+        splits = row_splits(d, max_k);
+        chunk = ((max_k + splits - 1) / splits + 63) / 64 * 64;
     }
     p.splits = static_cast<int>(std::max<int64_t>(1, splits));
     p.chunk = static_cast<int>(std::max<int64_t>(128, std::min<int64_t>(chunk, int64_t(1) << 30)));

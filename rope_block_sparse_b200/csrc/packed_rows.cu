@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedAr
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int found_nonfinite;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel, if there is one, may be set up
     // split slowest: the parts that short sequences do not have come last
     uint32_t at = blockIdx.x;
     const int kvh = at % a.kv_heads;

@@ -724,6 +724,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     Smem<G>& sm = *reinterpret_cast<Smem<G>*>(smem_raw + (((base + 1023u) & ~1023u) - base));
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel, if there is one, may be set up
     const int warp = threadIdx.x >> 5;
     if (warp == G::kMmaWarp) {
         tmem_alloc(&sm.tmem_base, G::kTmemCols);
