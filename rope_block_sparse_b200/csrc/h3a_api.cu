@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -222,7 +223,10 @@ uint64_t turns_of(double frequency) {
 }
 
 // Checks a packed descriptor and lays out its partial rows.
-h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, size_t* rows_bytes, size_t* bytes) {
+struct PackedRoom {
+    size_t o, lse, all;  // bytes of the partial rows, up to their log-sum-exps' end, and of everything
+};
+h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, PackedRoom* room) {
     if (d == nullptr || !known(d->dtype)) return H3A_ERR_INVALID_ARG;
     if (d->seqs < 1 || d->heads < 1 || d->kv_heads < 1 || d->heads % d->kv_heads) return H3A_ERR_INVALID_ARG;
     if (d->total_q < 0 || d->total_k < 0 || d->max_q < 0 || d->max_k < 0) return H3A_ERR_INVALID_ARG;
@@ -242,17 +246,20 @@ h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, size_t* rows
         return H3A_ERR_INVALID_ARG;
     *plan = packed_plan(*d);
     const int group = d->heads / d->kv_heads;
-    const double columns = plan->tiles ? static_cast<double>(packed_tile_groups(d->total_q, d->seqs, group, plan->tiles)) : d->seqs;
+    const double columns = plan->tiles ? static_cast<double>(packed_tile_groups(d->total_q, d->seqs, group, plan->tiles))
+                                       : std::max(d->seqs, plan->streams);
     // the tile kernel's grid has the kv heads as its second dimension
     const double grid = plan->tiles ? (d->kv_heads > 65535 ? static_cast<double>(lim) : columns)
-                                    : columns * d->kv_heads * plan->splits;
+                                    : columns * d->kv_heads;
     const double rows = static_cast<double>(d->total_q) * d->heads;
     if (grid >= static_cast<double>(lim) || rows >= static_cast<double>(lim)) return H3A_ERR_UNSUPPORTED;
-    *rows_bytes = *bytes = 0;
-    if (plan->splits > 1) {
-        const size_t parts = static_cast<size_t>(plan->splits) * static_cast<size_t>(d->total_q) * d->heads;
-        *rows_bytes = align256(parts * d->head_dim * sizeof(float));
-        *bytes = *rows_bytes + align256(parts * sizeof(float));
+    *room = PackedRoom{};
+    if (plan->splits > 1 || plan->streams > 0) {
+        const size_t parts = plan->streams > 0 ? static_cast<size_t>(plan->streams) * d->kv_heads * 2 * kRowSlots
+                                               : static_cast<size_t>(plan->splits) * static_cast<size_t>(d->total_q) * d->heads;
+        room->o = align256(parts * d->head_dim * sizeof(float));
+        room->lse = room->o + align256(parts * sizeof(float));
+        room->all = room->lse + (plan->streams > 0 ? align256(static_cast<size_t>(d->seqs) * sizeof(int2)) : 0);
     }
     return H3A_OK;
 }
@@ -551,11 +558,11 @@ h3a_status h3a_residual_rmsnorm(const void* x, int64_t x_stride, const void* f, 
 
 h3a_status h3a_packed_attention_workspace_size(const h3a_packed_desc* d, size_t* bytes) {
     PackedPlan plan;
-    size_t rows_bytes, all;
-    const h3a_status rc = packed_check(d, &plan, &rows_bytes, &all);
+    PackedRoom room;
+    const h3a_status rc = packed_check(d, &plan, &room);
     if (rc != H3A_OK) return rc;
     if (bytes == nullptr) return H3A_ERR_INVALID_ARG;
-    *bytes = all;
+    *bytes = room.all;
     return H3A_OK;
 }
 
@@ -563,8 +570,8 @@ h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, con
                                 const int32_t* starts_q, const int32_t* starts_k, const int32_t* lengths_k, void* o,
                                 float* lse, void* workspace, size_t ws_bytes, h3a_stream_t stream) {
     PackedPlan plan;
-    size_t rows_bytes, bytes;
-    h3a_status rc = packed_check(d, &plan, &rows_bytes, &bytes);
+    PackedRoom room;
+    h3a_status rc = packed_check(d, &plan, &room);
     if (rc != H3A_OK) return rc;
     if (d->total_q == 0 || d->max_q == 0) return H3A_OK;  // no query, nothing to write
     if (!q || !o || (d->total_k > 0 && (!k || !v)) || !starts_q || !starts_k) return H3A_ERR_INVALID_ARG;
@@ -572,7 +579,7 @@ h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, con
     for (const void* p : {static_cast<const void*>(starts_q), static_cast<const void*>(starts_k),
                           static_cast<const void*>(lengths_k), static_cast<const void*>(lse)})
         if (reinterpret_cast<uintptr_t>(p) & 3u) return H3A_ERR_INVALID_ARG;
-    if (bytes > 0 && (!workspace || !aligned16(workspace) || ws_bytes < bytes)) return H3A_ERR_WORKSPACE;
+    if (room.all > 0 && (!workspace || !aligned16(workspace) || ws_bytes < room.all)) return H3A_ERR_WORKSPACE;
     PackedArgs a{};
     a.q = q, a.k = k, a.v = v, a.o = o, a.lse = lse;
     a.starts_q = starts_q, a.starts_k = starts_k, a.lengths_k = lengths_k;
@@ -583,10 +590,11 @@ h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, con
     a.causal = d->causal != 0;
     const double scale = d->scale == 0.0f ? 1.0 / std::sqrt(static_cast<double>(d->head_dim)) : d->scale;
     a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-    a.splits = plan.splits, a.chunk = plan.chunk;
-    if (plan.splits > 1) {
+    a.splits = plan.splits, a.chunk = plan.chunk, a.streams = plan.streams;
+    if (room.all > 0) {
         a.part_o = static_cast<float*>(workspace);
-        a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes);
+        a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + room.o);
+        a.part_slots = reinterpret_cast<int2*>(static_cast<char*>(workspace) + room.lse);
     }
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
@@ -601,7 +609,7 @@ h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, con
     } else {
         e = launch_packed_rows(a, d->head_dim, d->dtype == H3A_FP16, st);
     }
-    if (e == cudaSuccess && plan.splits > 1) e = launch_packed_combine(a, d->head_dim, d->dtype == H3A_FP16, st);
+    if (e == cudaSuccess && room.all > 0) e = launch_packed_combine(a, d->head_dim, d->dtype == H3A_FP16, st);
     return e == cudaSuccess ? H3A_OK : cuda_fail(e);
 }
 

@@ -9,9 +9,6 @@
 #ifndef ONE_TILE_KEYS
 #define ONE_TILE_KEYS -1
 #endif
-#ifndef JOINUS
-#define JOINUS 3.0
-#endif
 namespace h3a {
 
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
@@ -33,19 +30,62 @@ int64_t packed_tile_groups(int64_t total_q, int seqs, int group, int tiles) {
 
 namespace {
 
-// Parts for the row kernel: what is estimated to end first.  Two CTAs a
-// multiprocessor take 64 keys in about 0.4 us each, a CTA's beginning and end
-// about 2 us; joining the parts is a second launch.
-int64_t row_splits(const h3a_packed_desc& d, int64_t max_k) {
-    const double base = static_cast<double>(d.seqs) * d.kv_heads, units = static_cast<double>((max_k + 63) / 64);
+// Parts for the tile kernel: what is estimated to end first.  With too few tiles
+// for the GPU, parts put the other multiprocessors to work; every part costs its
+// CTA a beginning and an end (about four 128-key steps), each of its rows an
+// fp32 row written and read, and the call a second launch.
+int64_t tile_splits(const h3a_packed_desc& d, int tiles, int64_t max_q, int64_t max_k) {
+    const int group = d.heads / d.kv_heads, span = tiles * packed_queries_per_tile(group);
+    const double slots = kSms * (tiles == 1 ? 2 : 1);
+    // every sequence's last CTA is half full on average
+    const double base = (static_cast<double>(d.total_q) / span + 0.5 * d.seqs) * d.kv_heads;
+    const double steps = static_cast<double>((max_k + 127) / 128);
+    // what a tile has to do on average: causal queries see what lies before them,
+    // and of several sequences most are shorter than the longest
+    double mean = d.causal && max_k > 0 ? steps * (1.0 - 0.5 * std::min(1.0, static_cast<double>(max_q) / max_k)) : steps;
+    if (d.seqs > 1) mean *= 0.6;
+    const double step_us = 1.8;
+    const double rows_us = static_cast<double>(d.total_q) * d.heads * d.head_dim * 8 / 4e6;
     int64_t best = 1;
     double least = 0;
-    for (int64_t s = 1; s <= 256 && s <= units; s += s < 16 ? 1 : s / 8) {
-        const double waves = std::max(1.0, base * s / (2 * kSms));
-        const double us = waves * (std::ceil(units / s) * 0.4 + 2.0) + (s > 1 ? JOINUS + 0.03 * s : 0.0);
-        if (s == 1 || us < 0.9 * least) {
+    for (int64_t s = 1; s <= 64 && (s == 1 || steps / s >= 2); ++s) {
+        const double longest = std::ceil(steps / s) + 4, waves = base * s / slots;
+        const double units = waves <= 1 ? longest : std::max(longest, waves * (mean / s + 4) + 0.5 * longest);
+        const double us = units * step_us + (s > 1 ? 4 + rows_us * s : 0);
+        // a clear gain only: the lengths are guessed, and tiles come in whole numbers
+        if (s == 1 || us < (best == 1 ? 0.75 : 0.95) * least) {
             best = s;
             least = us;
+        }
+    }
+    return best;
+}
+
+// Stretches that the row kernel's keys are cut into (packed_rows.cu), 0 for a CTA
+// a sequence and kv head: where that would leave the GPU idle for longer than
+// joining parts takes.
+int row_streams(const h3a_packed_desc& d, int64_t max_k) {
+    const double base = static_cast<double>(d.seqs) * d.kv_heads;
+    const int slots = kSms * packed_rows_ctas(d.head_dim);
+    const double blocks = static_cast<double>((max_k + 63) / 64);  // of the longest sequence
+    // A CTA takes 64 keys in 0.006 us a channel.  Around them 3 us, streamed 10 (the
+    // stretches to find and the second launch); ragged sequences are half as long
+    // as the longest on average.  Measured (us, a CTA each against streamed):
+    // 8 x 16 heads x 64 up to 900 keys 8.8 / 11.8, 1 x 8 x 64 of 2,000 15.3 / 8.8,
+    // 32 x 8 x 128 up to 700 16.3 / 22.7, 16 x 8 x 128 up to 3,000 39.0 / 26.8.
+    const double block_us = 0.006 * d.head_dim;
+    const double whole = 3 + std::max(1.0, base / slots) * blocks * block_us;
+    const double streamed = 10 + std::max(2.0, 0.5 * blocks * base / slots) * block_us;
+    if (whole <= streamed) return 0;
+    // one for each kv head: as many as fill one to three rounds of the GPU best
+    int best = 1;
+    double most = 0;
+    for (int rounds = 1; rounds <= 3; ++rounds) {
+        const int n = std::max(1, rounds * slots / d.kv_heads);
+        const double used = static_cast<double>(n) * d.kv_heads / (std::ceil(static_cast<double>(n) * d.kv_heads / slots) * slots);
+        if (used > most + 0.05) {
+            best = n;
+            most = used;
         }
     }
     return best;
@@ -64,22 +104,16 @@ PackedPlan packed_plan(const h3a_packed_desc& d) {
     // 16 prompts): 32/8 heads x 128 up to 300 keys 21.8 / 24.1, 700 51.6 / 53.1, 1,000
     // 77.9 / 76.8; 28/4 x 96 up to 700 40.3 / 41.1, 1,000 60.5 / 59.2; 16 x 64 up to
     // 2,000 87.9 / 98.3, but one prompt of 16,000 792 / 771.
-    const int64_t one_tile = ONE_TILE_KEYS >= 0 ? ONE_TILE_KEYS : d.head_dim == 64 ? 4096 : 768;
-    p.tiles = max_q * group <= 16 ? 0 : max_k <= one_tile ? 1 : 2;
-    int64_t splits, chunk;
+    const int64_t one_tile = d.head_dim == 64 ? 4096 : 768;
+    p.tiles = max_q * group <= kRowSlots ? 0 : max_k <= one_tile ? 1 : 2;
+    int64_t splits = 1, chunk = max_k;
     if (p.tiles) {
-        // a part for every multiprocessor without work, each of at least 512
-        // keys (a part costs each of its rows an fp32 row written and read)
-        const int64_t pairs = std::max<int64_t>(1, (d.total_q + 2 * packed_queries_per_tile(group) - 1) / (2 * packed_queries_per_tile(group)));
-        const int64_t work = pairs * d.kv_heads;
-        splits = std::min(kSms / std::max<int64_t>(work, 1), max_k / 512);
-        splits = std::max<int64_t>(1, std::min<int64_t>(splits, 64));
+        splits = tile_splits(d, p.tiles, max_q, max_k);
         chunk = ((max_k + splits - 1) / splits + 127) / 128 * 128;
     } else {
-        splits = row_splits(d, max_k);
-        chunk = ((max_k + splits - 1) / splits + 63) / 64 * 64;
+        p.streams = row_streams(d, max_k);
     }
-    p.splits = static_cast<int>(std::max<int64_t>(1, splits));
+    p.splits = static_cast<int>(splits);
     p.chunk = static_cast<int>(std::max<int64_t>(128, std::min<int64_t>(chunk, int64_t(1) << 30)));
     return p;
 }

@@ -3,25 +3,33 @@
 // calls with more rows).
 //
 // The queries that share a kv head are the rows of one matrix: row r of a
-// sequence is query r / group, head r % group of the kv head's group.  A CTA
-// takes all of them, at most 16 (the M of mma.m16n8k16), and one part of the
-// sequence's keys;
-// its warps take units of 16 keys in turn, each with a cp.async pipeline of its
-// own through shared memory, so no barrier stands between load and use:
+// sequence is query r / group, head r % group of the kv head's group, at most
+// 16 (the M of mma.m16n8k16).  A CTA's warps take units of 16 keys in turn, each
+// with a cp.async pipeline of its own through shared memory, so no barrier
+// stands between load and use:
 //   S = Q K^T (Q in registers), online softmax in fp32 (log2 domain, running
 //   row maximum m and sum l), O = alpha O + P V with P rounded to the element
 //   type straight from S's registers.
-// At the end the warps' (m, l, O) are joined through shared memory, and, when
-// the keys were split over CTAs, written as a normalised fp32 row with its
-// log-sum-exp for packed_combine.cu.  HBM-bound: K and V are read once;
-// one unit is 16 keys x (K + V) = 8 KB at head_dim 128.
+// At the end the warps' (m, l, O) are joined through shared memory.  HBM-bound:
+// K and V are read once; one unit is 16 keys x (K + V) = 8 KB at head_dim 128.
 //
-// Keys no row of the CTA attends are read as zeros (cp.async with a source
-// size of 0), so what lies behind a sequence is never touched.  Where some rows
-// attend a key and others do not (causal, several queries), an infinity or NaN
-// in V would reach the others as 0 * NaN: such a unit's V fragments have their
-// non-finite values set to zero, and the epilogue adds those back to exactly
-// the rows that attend them.
+// Work: blocks of 64 keys of all sequences, one behind the other.  Short
+// sequences get a CTA each (and kv head).  Long or few ones are streamed: the
+// blocks are cut into equal stretches, whatever sequences they run through, as
+// many as make the GPU's CTAs with one for each kv head, so that neither a long
+// sequence nor a short batch leaves part of the GPU idle; a sequence that lies
+// in one stretch is finished there, the others' parts go to the workspace and
+// are joined by packed_combine.cu.  The kv heads of a stretch run side by side:
+// their rows of a key lie behind one another in memory, and apart in time they
+// are 256 bytes here and there (16,000 keys of 8 kv heads x 128 by stretches of
+// single heads: 20.5 us, side by side STREAM_US).
+//
+// Keys no row attends are read as zeros (cp.async with a source size of 0), so
+// what lies behind a sequence is never touched.  Where some rows attend a key
+// and others do not (causal, several queries), an infinity or NaN in V would
+// reach the others as 0 * NaN: such a unit's V fragments have their non-finite
+// values set to zero, and the end adds those back to exactly the rows that
+// attend them.
 #include "half16.cuh"
 #include "prompt_internal.h"
 
@@ -31,7 +39,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 16;    // keys a warp takes at a time
-constexpr int kStages = 3;
+// One unit on its way while one is in work: 2 CTAs x 4 warps x 8 KB = 64 KB a
+// multiprocessor cover the latency, and more requests at a time only disturb one
+// another (47 caches of up to 16,384 keys: 183 us; with two units on their way 198,
+// with three 203).
+constexpr int kStages = 2;
 
 template <int D>
 struct Geo {
@@ -89,30 +101,34 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+constexpr int kBlockKeys = kUnit * kWarps;  // 64: what the work is counted in
+
+// Queries of the sequence that count, and blocks of its keys that any of them attends.
+__device__ __forceinline__ int counted_queries(const PackedArgs& a, const PackedSeq& s) {
+    return static_cast<int>(min(static_cast<int64_t>(s.lq), a.max_q));
+}
+__device__ __forceinline__ int key_blocks(const PackedArgs& a, const PackedSeq& s) {
+    const int queries = counted_queries(a, s);
+    return queries == 0 ? 0 : (packed_limit(a, s, queries - 1) + kBlockKeys - 1) / kBlockKeys;
+}
+
+// Keys [begin, end) of one (sequence, kv head), and where the result goes.
+struct Segment {
+    int kvh, begin, end;
+    int64_t slot;  // part's slot, or -1: the end result
+};
+
+// found[2]: a warp cleared a value of V, in turns (0 at the first call) so that one
+// is set back while nobody uses it.
 template <int D, bool FP16>
-__global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedArgs a) {
+__device__ __forceinline__ void attend(const PackedArgs& a, const PackedSeq& s, const Segment& g, uint8_t* smem, int* found, int turn) {
     using G = Geo<D>;
     using H = Half16<FP16>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int found_nonfinite;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel, if there is one, may be set up
-    // split slowest: the parts that short sequences do not have come last
-    uint32_t at = blockIdx.x;
-    const int kvh = at % a.kv_heads;
-    at /= a.kv_heads;
-    const int seq = at % a.seqs, split = at / a.seqs;
-    const PackedSeq s = packed_seq(a, seq);
-    const int queries = static_cast<int>(min(static_cast<int64_t>(s.lq), a.max_q));
+    const int queries = counted_queries(a, s);
     const int rows = queries * a.group;  // at most 16
-    if (rows == 0) return;
-    const int least = packed_limit(a, s, 0), most = packed_limit(a, s, queries - 1);
-    // this part's keys; the last part takes what remains, the first is never left out
-    const int begin = split == 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(split) * a.chunk, static_cast<int64_t>(most)));
-    const int end = split + 1 == a.splits ? most : static_cast<int>(min((split + 1) * static_cast<int64_t>(a.chunk), static_cast<int64_t>(most)));
-    if (split > 0 && begin >= end) return;  // the combine does not read parts past a row's keys
-    if (threadIdx.x == 0) found_nonfinite = 0;
-    __syncthreads();
+    const int least = packed_limit(a, s, 0);
+    const int begin = g.begin, end = g.end, kvh = g.kvh;
 
     // Q: rows lane / 4 and lane / 4 + 8 of the A fragments
     const int ra = lane >> 2;
@@ -241,8 +257,9 @@ __global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedAr
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
     }
-    if (nonfinite) found_nonfinite = 1;
+    if (nonfinite) found[turn] = 1;
     __syncthreads();  // every warp is done with its pipeline: the join reuses it
+    if (threadIdx.x == 0) found[turn ^ 1] = 0;
     float* jo = reinterpret_cast<float*>(smem);
     float* jm = jo + kWarps * 16 * G::kJoinPitch;
     float* jl = jm + kWarps * 16;
@@ -262,67 +279,155 @@ __global__ void __launch_bounds__(kThreads, 2) packed_rows_kernel(const PackedAr
     __syncthreads();
     // eight threads a row, every eighth group of four channels each
     const int row = threadIdx.x >> 3;
-    if (row >= rows) return;
-    const int query = row / a.group;
-    const int64_t n = s.q0 + query;
-    const int head = kvh * a.group + row % a.group;
-    float top = -INFINITY, w[kWarps], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, jm[i * 16 + row]);
-    const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        w[i] = exp2_fast(jm[i * 16 + row] - ref);
-        sum += w[i] * jl[i * 16 + row];
-    }
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    const float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
-    const int64_t qh = n * a.heads + head;
-    const int limit_row = min(packed_limit(a, s, query), end);
-    for (int c = (threadIdx.x & 7) * 4; c < D; c += 32) {
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
+    if (row < rows) {
+        const int query = row / a.group;
+        const int64_t n = s.q0 + query;
+        const int head = kvh * a.group + row % a.group;
+        float top = -INFINITY, w[kWarps], sum = 0.f;
+    #pragma unroll
+        for (int i = 0; i < kWarps; ++i) top = fmaxf(top, jm[i * 16 + row]);
+        const float ref = top == -INFINITY ? 0.f : top;
+    #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(jo + (i * 16 + row) * G::kJoinPitch + c);
-            acc.x = fmaf(w[i], v.x, acc.x), acc.y = fmaf(w[i], v.y, acc.y);
-            acc.z = fmaf(w[i], v.z, acc.z), acc.w = fmaf(w[i], v.w, acc.w);
+            w[i] = exp2_fast(jm[i * 16 + row] - ref);
+            sum += w[i] * jl[i * 16 + row];
         }
-        acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-        if (found_nonfinite) {
-            // the units whose V was cleared: from the first key some row does not attend
-            const int from = max(begin, begin + (least - begin) / kUnit * kUnit);
-            for (int key = from; key < limit_row; ++key) {
-                const uint2 raw = *reinterpret_cast<const uint2*>(vbase + static_cast<int64_t>(key) * a.vn + c);
-                float x[4];
-                H::unpack(raw.x, x[0], x[1]);
-                H::unpack(raw.y, x[2], x[3]);
-                acc.x += isfinite(x[0]) ? 0.f : x[0], acc.y += isfinite(x[1]) ? 0.f : x[1];
-                acc.z += isfinite(x[2]) ? 0.f : x[2], acc.w += isfinite(x[3]) ? 0.f : x[3];
+        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+        const float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
+        const int64_t qh = n * a.heads + head;
+        const int limit_row = min(packed_limit(a, s, query), end);
+        for (int c = (threadIdx.x & 7) * 4; c < D; c += 32) {
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    #pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float4 v = *reinterpret_cast<const float4*>(jo + (i * 16 + row) * G::kJoinPitch + c);
+                acc.x = fmaf(w[i], v.x, acc.x), acc.y = fmaf(w[i], v.y, acc.y);
+                acc.z = fmaf(w[i], v.z, acc.z), acc.w = fmaf(w[i], v.w, acc.w);
+            }
+            acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+            if (found[turn]) {
+                // the units whose V was cleared: from the first key some row does not attend
+                const int from = max(begin, begin + (least - begin) / kUnit * kUnit);
+                for (int key = from; key < limit_row; ++key) {
+                    const uint2 raw = *reinterpret_cast<const uint2*>(vbase + static_cast<int64_t>(key) * a.vn + c);
+                    float x[4];
+                    H::unpack(raw.x, x[0], x[1]);
+                    H::unpack(raw.y, x[2], x[3]);
+                    acc.x += isfinite(x[0]) ? 0.f : x[0], acc.y += isfinite(x[1]) ? 0.f : x[1];
+                    acc.z += isfinite(x[2]) ? 0.f : x[2], acc.w += isfinite(x[3]) ? 0.f : x[3];
+                }
+            }
+            if (g.slot >= 0) {
+                *reinterpret_cast<float4*>(a.part_o + (g.slot * kRowSlots + row) * D + c) = acc;
+            } else {
+                uint16_t* dst = static_cast<uint16_t*>(a.o) + n * a.on + head * a.oh + c;
+                *reinterpret_cast<uint2*>(dst) = make_uint2(H::pack(acc.x, acc.y), H::pack(acc.z, acc.w));
             }
         }
-        if (a.splits > 1) {
-            *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(split) * a.total_q * a.heads + qh) * D + c) = acc;
-        } else {
-            uint16_t* dst = static_cast<uint16_t*>(a.o) + n * a.on + head * a.oh + c;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(H::pack(acc.x, acc.y), H::pack(acc.z, acc.w));
+        if ((threadIdx.x & 7) == 0) {
+            if (g.slot >= 0)
+                a.part_lse[g.slot * kRowSlots + row] = lse2;
+            else if (a.lse)
+                a.lse[qh] = lse2 * 0.6931471805599453f;
         }
     }
-    if ((threadIdx.x & 7) == 0) {
-        if (a.splits > 1)
-            a.part_lse[static_cast<int64_t>(split) * a.total_q * a.heads + qh] = lse2;
-        else if (a.lse)
-            a.lse[qh] = lse2 * 0.6931471805599453f;
+    __syncthreads();  // the next segment reuses the shared memory
+}
+
+// A CTA a (sequence, kv head).
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, packed_rows_ctas(D)) packed_rows_kernel(const __grid_constant__ PackedArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int found[2];
+    if (threadIdx.x == 0) found[0] = found[1] = 0;
+    __syncthreads();
+    const PackedSeq s = packed_seq(a, blockIdx.x / a.kv_heads);
+    const int queries = counted_queries(a, s);
+    if (queries == 0) return;
+    attend<D, FP16>(a, s, {static_cast<int>(blockIdx.x % a.kv_heads), 0, packed_limit(a, s, queries - 1), -1}, smem, found, 0);
+}
+
+// An equal stretch of all key blocks a CTA.
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, packed_rows_ctas(D)) packed_stream_kernel(const __grid_constant__ PackedArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int found[2];
+    __shared__ int64_t sums[kWarps];
+    __shared__ int64_t start_blocks;  // blocks before the sequence the stretch starts in
+    __shared__ int start_seq;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be set up
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // Blocks of all sequences: each thread counts a run of them, then a scan.
+    const int run = (a.seqs + kThreads - 1) / kThreads;
+    const int first = threadIdx.x * run, last = min(first + run, a.seqs);
+    int64_t mine = 0;
+    for (int i = first; i < last; ++i) mine += key_blocks(a, packed_seq(a, i));
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    if (threadIdx.x == 0) found[0] = found[1] = 0;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) upto += sums[i];
+        all += sums[i];
+    }
+    // two blocks at least: a stretch has a beginning and an end
+    const int64_t stretch = max((all + a.streams - 1) / a.streams, int64_t(2));
+    const int kvh = blockIdx.x % a.kv_heads, stream = blockIdx.x / a.kv_heads;
+    int64_t at = stream * stretch;
+    const int64_t to = min(at + stretch, all);
+    if (at >= to) return;
+    if (upto - mine <= at && at < upto) {
+        int64_t before = upto - mine;
+        int i = first;
+        for (;; ++i) {
+            const int n = key_blocks(a, packed_seq(a, i));
+            if (at < before + n) break;
+            before += n;
+        }
+        start_seq = i;
+        start_blocks = before;
+    }
+    __syncthreads();
+    int seq = start_seq;
+    PackedSeq s = packed_seq(a, seq);
+    int blocks = key_blocks(a, s);
+    int block = static_cast<int>(at - start_blocks);
+    for (int slot = 0, turn = 0;; slot = 1, turn ^= 1) {
+        const int count = static_cast<int>(min(static_cast<int64_t>(blocks - block), to - at));
+        const int end = min((block + count) * kBlockKeys, packed_limit(a, s, counted_queries(a, s) - 1));
+        // only a stretch's first and last sequence can be a part
+        const int part = count == blocks ? -1 : stream * 2 + slot;
+        attend<D, FP16>(a, s, {kvh, block * kBlockKeys, end, part < 0 ? -1 : packed_part_slot(a, part, kvh)}, smem, found, turn);
+        if (threadIdx.x == 0 && kvh == 0) {
+            if (block == 0) a.part_slots[seq].x = part;
+            if (block + count == blocks) a.part_slots[seq].y = part;
+        }
+        at += count;
+        if (at >= to) return;
+        block = 0;
+        do {  // there are blocks left, so a sequence that has some follows
+            s = packed_seq(a, ++seq);
+            blocks = key_blocks(a, s);
+        } while (blocks == 0);
     }
 }
 
 template <int D, bool FP16>
 cudaError_t run(const PackedArgs& a, cudaStream_t st) {
     constexpr int smem = Geo<D>::kSmem;
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(packed_rows_kernel<D, FP16>), smem, done);
+    static std::atomic<uint64_t> done[2]{};
+    const auto kernel = a.streams > 0 ? packed_stream_kernel<D, FP16> : packed_rows_kernel<D, FP16>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done[a.streams > 0]);
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(a.seqs) * a.kv_heads * a.splits;
-    packed_rows_kernel<D, FP16><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
+    const int64_t grid = static_cast<int64_t>(a.streams > 0 ? a.streams : a.seqs) * a.kv_heads;
+    kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 

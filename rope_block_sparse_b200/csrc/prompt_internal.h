@@ -57,10 +57,19 @@ struct PackedArgs {
     int seqs, heads, kv_heads, group;
     int causal;
     float scale_log2;  // logit scale * log2(e)
-    int splits;        // parts a sequence's keys may be cut into
-    int chunk;         // keys of each part (the last part takes what remains)
-    float* part_o;     // [splits, total_q, heads, d] when splits > 1: normalised rows
-    float* part_lse;   // [splits, total_q, heads], log2 units
+    // Parts of sequences' keys, joined by launch_packed_combine: normalised fp32
+    // rows and their log-sum-exps (log2 units).
+    // Tile kernel: parts of `chunk` keys (the last of `splits` takes what
+    // remains), row (split * total_q + query) * heads + head.
+    // Row kernel: `streams` stretches of all keys (0: a CTA takes whole sequences
+    // and nothing is joined) have two parts each, 2 i of the sequence in which
+    // stretch i begins and 2 i + 1 of the one in which it ends, kRowSlots rows for
+    // every kv head; part_slots has each sequence's first and last part, or -1
+    // when it needs no joining.
+    int splits, chunk, streams;
+    float* part_o;
+    float* part_lse;
+    int2* part_slots;
 };
 // What a sequence's entry of the index arrays means, cut to the tensors.
 struct PackedSeq {
@@ -88,17 +97,25 @@ __device__ __forceinline__ int packed_limit(const PackedArgs& a, const PackedSeq
     return static_cast<int>(min(max(n, int64_t(0)), static_cast<int64_t>(s.lk)));
 }
 
+constexpr int kRowSlots = 16;  // rows of a part of the row kernel
+// Where the row kernel's part is, in units of kRowSlots rows.
+__device__ __forceinline__ int64_t packed_part_slot(const PackedArgs& a, int part, int kvh) {
+    return static_cast<int64_t>(part) * a.kv_heads + kvh;
+}
+
 // How a call is carried out (packed_plan.cu).
 struct PackedPlan {
     int tiles;  // 128-row tiles a CTA on tcgen05 (packed_tiles.cu): 1 or 2; 0: 16 rows (packed_rows.cu)
-    int splits, chunk;
+    int splits, chunk, streams;
 };
 PackedPlan packed_plan(const h3a_packed_desc& d);
+// CTAs of the row kernel that a multiprocessor holds.
+constexpr int packed_rows_ctas(int d) { return d == 64 ? 4 : 2; }
 // Queries in a 128-row tile, and the CTAs of `tiles` tiles that hold every sequence's.
 int packed_queries_per_tile(int group);
 int64_t packed_tile_groups(int64_t total_q, int seqs, int group, int tiles);
 
-// At most 16 rows (queries x group) of each sequence and kv head.
+// At most kRowSlots rows (queries x group) of each sequence and kv head.
 cudaError_t launch_packed_rows(const PackedArgs& a, int d, bool fp16, cudaStream_t st);
 // Tensor maps: q as {d, group, kv_heads, total_q} with a {32, group, 1,
 // packed_queries_per_tile} box, k and v as {d, kv_heads, total_k} with {32, 1,

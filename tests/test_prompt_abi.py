@@ -118,10 +118,12 @@ def test_packed_workspace_size():
         return n.value
 
     assert size(max_k=100) == 0                                  # one part: nothing to join
-    parts = size(seqs=1, total_q=1, max_q=1, total_k=100000, max_k=100000)
-    rows = parts / (8 * (128 + 1) * 4)
-    assert parts % 256 == 0 and 2 <= rows <= 257                 # at most 256 parts of a row and its log-sum-exp
-    assert size(max_q=0) == size(max_q=0)
+    # a single token over a long cache: two parts of 16 rows with their log-sum-exps for each of two CTAs a
+    # multiprocessor (148), and a pair of numbers for the sequence
+    assert size(seqs=1, total_q=1, max_q=1, total_k=100000, max_k=100000) == 148 * 2 * 2 * 16 * (128 + 1) * 4 + 256
+    # a piece of a prompt behind a long cache: whole parts of every row
+    parts = size(seqs=1, total_q=64, max_q=64, total_k=100000, max_k=100000)
+    assert parts % (64 * 8 * (128 + 1) * 4) == 0 and 2 <= parts // (64 * 8 * (128 + 1) * 4) <= 64
     assert lib.h3a_packed_attention_workspace_size(packed(), None) == 1
     assert lib.h3a_packed_attention_workspace_size(None, n) == 1
 
