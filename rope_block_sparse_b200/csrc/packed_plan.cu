@@ -68,14 +68,17 @@ int row_streams(const h3a_packed_desc& d, int64_t max_k) {
     const double base = static_cast<double>(d.seqs) * d.kv_heads;
     const int slots = kSms * packed_rows_ctas(d.head_dim);
     const double blocks = static_cast<double>((max_k + 63) / 64);  // of the longest sequence
-    // A CTA takes 64 keys in 0.006 us a channel.  Around them 3 us, streamed 10 (the
-    // stretches to find and the second launch); ragged sequences are half as long
-    // as the longest on average.  Measured (us, a CTA each against streamed):
-    // 8 x 16 heads x 64 up to 900 keys 8.8 / 11.8, 1 x 8 x 64 of 2,000 15.3 / 8.8,
-    // 32 x 8 x 128 up to 700 16.3 / 22.7, 16 x 8 x 128 up to 3,000 39.0 / 26.8.
+    // A CTA takes 64 keys in 0.006 us a channel, one of eight warps in 0.8 of it.
+    // Around them 3 us, streamed 8 to 11 (the stretches to find, the second
+    // launch, more ends with more sequences); ragged sequences are half as long as
+    // the longest on average.  Measured (us, a CTA each against streamed): 8
+    // sequences x 16 heads x 64 up to 900 keys 7.6 / 11.8, 1 x 8 x 64 of 2,000 12.1 /
+    // 8.0, 16 x 8 x 128 up to 700 10.8 / 12.6, up to 3,000 28.1 / 24.3, 1 x 8 x 128 of
+    // 4,000 41.1 / 10.6.
     const double block_us = 0.006 * d.head_dim;
-    const double whole = 3 + std::max(1.0, base / slots) * blocks * block_us;
-    const double streamed = 10 + std::max(2.0, 0.5 * blocks * base / slots) * block_us;
+    const double few = packed_rows_few(d.head_dim, static_cast<int64_t>(base)) ? 0.8 : 1.0;
+    const double whole = 3 + std::max(1.0, base / slots) * blocks * block_us * few;
+    const double streamed = 8 + 3 * std::min(1.0, base / 64) + std::max(2.0, 0.5 * blocks * base / slots) * block_us;
     if (whole <= streamed) return 0;
     // one for each kv head: as many as fill one to three rounds of the GPU best
     int best = 1;

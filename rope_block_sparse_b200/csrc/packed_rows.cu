@@ -22,7 +22,7 @@
 // are joined by packed_combine.cu.  The kv heads of a stretch run side by side:
 // their rows of a key lie behind one another in memory, and apart in time they
 // are 256 bytes here and there (16,000 keys of 8 kv heads x 128 by stretches of
-// single heads: 20.5 us, side by side STREAM_US).
+// single heads: 20.5 us, side by side 16).
 //
 // Keys no row attends are read as zeros (cp.async with a source size of 0), so
 // what lies behind a sequence is never touched.  Where some rows attend a key
@@ -36,8 +36,7 @@
 namespace h3a {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 4;    // of a streamed CTA
 constexpr int kUnit = 16;    // keys a warp takes at a time
 // One unit on its way while one is in work: 2 CTAs x 4 warps x 8 KB = 64 KB a
 // multiprocessor cover the latency, and more requests at a time only disturb one
@@ -45,15 +44,16 @@ constexpr int kUnit = 16;    // keys a warp takes at a time
 // with three 203).
 constexpr int kStages = 2;
 
-template <int D>
+// A CTA of W warps.
+template <int D, int W>
 struct Geo {
     static constexpr int kPitch = D * 2 + 16;  // an odd multiple of 16 bytes: ldmatrix rows hit distinct banks
     static constexpr int kTile = kUnit * kPitch;
     static constexpr int kChunks = D / 8;      // 16-byte chunks of a key
     static constexpr int kStageBytes = 2 * kTile;
-    static constexpr int kPipeBytes = kWarps * kStages * kStageBytes;
+    static constexpr int kPipeBytes = W * kStages * kStageBytes;
     static constexpr int kJoinPitch = D + 4;
-    static constexpr int kJoinBytes = (kWarps * 16 * kJoinPitch + kWarps * 16 * 2) * 4;
+    static constexpr int kJoinBytes = (W * 16 * kJoinPitch + W * 16 * 2) * 4;
     static constexpr int kSmem = kPipeBytes > kJoinBytes ? kPipeBytes : kJoinBytes;
     static_assert(D % 16 == 0 && (kUnit * kChunks) % 32 == 0, "head_dim");
 };
@@ -120,9 +120,9 @@ struct Segment {
 
 // found[2]: a warp cleared a value of V, in turns (0 at the first call) so that one
 // is set back while nobody uses it.
-template <int D, bool FP16>
+template <int D, bool FP16, int W>
 __device__ __forceinline__ void attend(const PackedArgs& a, const PackedSeq& s, const Segment& g, uint8_t* smem, int* found, int turn) {
-    using G = Geo<D>;
+    using G = Geo<D, W>;
     using H = Half16<FP16>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int queries = counted_queries(a, s);
@@ -174,7 +174,7 @@ __device__ __forceinline__ void attend(const PackedArgs& a, const PackedSeq& s, 
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     bool nonfinite = false;
-    constexpr int kStride = kUnit * kWarps;
+    constexpr int kStride = kUnit * W;
     int next = begin + warp * kUnit;
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i, next += kStride) load(next, i);
@@ -261,8 +261,8 @@ __device__ __forceinline__ void attend(const PackedArgs& a, const PackedSeq& s, 
     __syncthreads();  // every warp is done with its pipeline: the join reuses it
     if (threadIdx.x == 0) found[turn ^ 1] = 0;
     float* jo = reinterpret_cast<float*>(smem);
-    float* jm = jo + kWarps * 16 * G::kJoinPitch;
-    float* jl = jm + kWarps * 16;
+    float* jm = jo + W * 16 * G::kJoinPitch;
+    float* jl = jm + W * 16;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
         float* d = jo + (warp * 16 + ra) * G::kJoinPitch + i * 8 + 2 * (lane & 3);
@@ -277,18 +277,19 @@ __device__ __forceinline__ void attend(const PackedArgs& a, const PackedSeq& s, 
         }
     }
     __syncthreads();
-    // eight threads a row, every eighth group of four channels each
-    const int row = threadIdx.x >> 3;
+    // 2 W threads a row, every 2 W-th group of four channels each
+    constexpr int kTeam = 2 * W;
+    const int row = threadIdx.x / kTeam;
     if (row < rows) {
         const int query = row / a.group;
         const int64_t n = s.q0 + query;
         const int head = kvh * a.group + row % a.group;
-        float top = -INFINITY, w[kWarps], sum = 0.f;
+        float top = -INFINITY, w[W], sum = 0.f;
     #pragma unroll
-        for (int i = 0; i < kWarps; ++i) top = fmaxf(top, jm[i * 16 + row]);
+        for (int i = 0; i < W; ++i) top = fmaxf(top, jm[i * 16 + row]);
         const float ref = top == -INFINITY ? 0.f : top;
     #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
+        for (int i = 0; i < W; ++i) {
             w[i] = exp2_fast(jm[i * 16 + row] - ref);
             sum += w[i] * jl[i * 16 + row];
         }
@@ -296,10 +297,10 @@ __device__ __forceinline__ void attend(const PackedArgs& a, const PackedSeq& s, 
         const float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
         const int64_t qh = n * a.heads + head;
         const int limit_row = min(packed_limit(a, s, query), end);
-        for (int c = (threadIdx.x & 7) * 4; c < D; c += 32) {
+        for (int c = (threadIdx.x % kTeam) * 4; c < D; c += 4 * kTeam) {
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
+            for (int i = 0; i < W; ++i) {
                 const float4 v = *reinterpret_cast<const float4*>(jo + (i * 16 + row) * G::kJoinPitch + c);
                 acc.x = fmaf(w[i], v.x, acc.x), acc.y = fmaf(w[i], v.y, acc.y);
                 acc.z = fmaf(w[i], v.z, acc.z), acc.w = fmaf(w[i], v.w, acc.w);
@@ -324,7 +325,7 @@ __device__ __forceinline__ void attend(const PackedArgs& a, const PackedSeq& s, 
                 *reinterpret_cast<uint2*>(dst) = make_uint2(H::pack(acc.x, acc.y), H::pack(acc.z, acc.w));
             }
         }
-        if ((threadIdx.x & 7) == 0) {
+        if (threadIdx.x % kTeam == 0) {
             if (g.slot >= 0)
                 a.part_lse[g.slot * kRowSlots + row] = lse2;
             else if (a.lse)
@@ -335,8 +336,8 @@ __device__ __forceinline__ void attend(const PackedArgs& a, const PackedSeq& s, 
 }
 
 // A CTA a (sequence, kv head).
-template <int D, bool FP16>
-__global__ void __launch_bounds__(kThreads, packed_rows_ctas(D)) packed_rows_kernel(const __grid_constant__ PackedArgs a) {
+template <int D, bool FP16, int W>
+__global__ void __launch_bounds__(32 * W, W == kWarps ? packed_rows_ctas(D) : 1) packed_rows_kernel(const __grid_constant__ PackedArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int found[2];
     if (threadIdx.x == 0) found[0] = found[1] = 0;
@@ -344,12 +345,12 @@ __global__ void __launch_bounds__(kThreads, packed_rows_ctas(D)) packed_rows_ker
     const PackedSeq s = packed_seq(a, blockIdx.x / a.kv_heads);
     const int queries = counted_queries(a, s);
     if (queries == 0) return;
-    attend<D, FP16>(a, s, {static_cast<int>(blockIdx.x % a.kv_heads), 0, packed_limit(a, s, queries - 1), -1}, smem, found, 0);
+    attend<D, FP16, W>(a, s, {static_cast<int>(blockIdx.x % a.kv_heads), 0, packed_limit(a, s, queries - 1), -1}, smem, found, 0);
 }
 
 // An equal stretch of all key blocks a CTA.
 template <int D, bool FP16>
-__global__ void __launch_bounds__(kThreads, packed_rows_ctas(D)) packed_stream_kernel(const __grid_constant__ PackedArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, packed_rows_ctas(D)) packed_stream_kernel(const __grid_constant__ PackedArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int found[2];
     __shared__ int64_t sums[kWarps];
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, packed_rows_ctas(D)) packed_stream_k
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be set up
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // Blocks of all sequences: each thread counts a run of them, then a scan.
-    const int run = (a.seqs + kThreads - 1) / kThreads;
+    const int run = (a.seqs + (32 * kWarps) - 1) / (32 * kWarps);
     const int first = threadIdx.x * run, last = min(first + run, a.seqs);
     int64_t mine = 0;
     for (int i = first; i < last; ++i) mine += key_blocks(a, packed_seq(a, i));
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, packed_rows_ctas(D)) packed_stream_k
         const int end = min((block + count) * kBlockKeys, packed_limit(a, s, counted_queries(a, s) - 1));
         // only a stretch's first and last sequence can be a part
         const int part = count == blocks ? -1 : stream * 2 + slot;
-        attend<D, FP16>(a, s, {kvh, block * kBlockKeys, end, part < 0 ? -1 : packed_part_slot(a, part, kvh)}, smem, found, turn);
+        attend<D, FP16, kWarps>(a, s, {kvh, block * kBlockKeys, end, part < 0 ? -1 : packed_part_slot(a, part, kvh)}, smem, found, turn);
         if (threadIdx.x == 0 && kvh == 0) {
             if (block == 0) a.part_slots[seq].x = part;
             if (block + count == blocks) a.part_slots[seq].y = part;
@@ -419,16 +420,26 @@ __global__ void __launch_bounds__(kThreads, packed_rows_ctas(D)) packed_stream_k
     }
 }
 
+template <int D, bool FP16, int W, bool STREAM>
+cudaError_t launch(const PackedArgs& a, cudaStream_t st) {
+    constexpr int smem = Geo<D, W>::kSmem;
+    static std::atomic<uint64_t> done{0};
+    constexpr auto kernel = STREAM ? packed_stream_kernel<D, FP16> : packed_rows_kernel<D, FP16, W>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(STREAM ? a.streams : a.seqs) * a.kv_heads;
+    kernel<<<static_cast<unsigned>(grid), 32 * W, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <int D, bool FP16>
 cudaError_t run(const PackedArgs& a, cudaStream_t st) {
-    constexpr int smem = Geo<D>::kSmem;
-    static std::atomic<uint64_t> done[2]{};
-    const auto kernel = a.streams > 0 ? packed_stream_kernel<D, FP16> : packed_rows_kernel<D, FP16>;
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done[a.streams > 0]);
-    if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(a.streams > 0 ? a.streams : a.seqs) * a.kv_heads;
-    kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    if (a.streams > 0) return launch<D, FP16, kWarps, true>(a, st);
+    // Few CTAs: each takes its keys faster with more warps (us, four warps against
+    // eight: 8 x 16 heads x 64 up to 900 keys 8.95 / 7.63, 16 x 8 x 128 up to 700
+    // 12.3 / 10.8, but 16 x 16 x 128, 256 CTAs, 13.9 / 15.8)
+    if (packed_rows_few(D, static_cast<int64_t>(a.seqs) * a.kv_heads)) return launch<D, FP16, 8, false>(a, st);
+    return launch<D, FP16, kWarps, false>(a, st);
 }
 
 }  // namespace

@@ -111,6 +111,8 @@ struct PackedPlan {
 PackedPlan packed_plan(const h3a_packed_desc& d);
 // CTAs of the row kernel that a multiprocessor holds.
 constexpr int packed_rows_ctas(int d) { return d == 64 ? 4 : 2; }
+// Whether so few CTAs of whole sequences take eight warps each.
+constexpr bool packed_rows_few(int d, int64_t ctas) { return ctas <= kSms * (d == 64 ? 2 : 1); }
 // Queries in a 128-row tile, and the CTAs of `tiles` tiles that hold every sequence's.
 int packed_queries_per_tile(int group);
 int64_t packed_tile_groups(int64_t total_q, int seqs, int group, int tiles);
