@@ -5,6 +5,11 @@
  *   h3a_qk_norm_rope  fused QK-RMSNorm + 3D RoPE over Q and K
  *   h3a_route         blockwise KV-block router (pool -> fp32 scores -> top-k)
  *   h3a_attention     bidirectional attention, dense or over routed KV blocks
+ * and, for the text model that conditions it, the prompt side (conventions of
+ * its own further down):
+ *   h3a_residual_rmsnorm  residual addition + RMS norm, to 16 or 8 bits
+ *   h3a_rope              one-dimensional rotary positions
+ *   h3a_packed_attention  causal attention over packed prompts and caches
  *
  * Conventions shared by every call
  *   - Tensors are bf16 (raw 16-bit words), laid out [B, N, heads, head_dim]
@@ -351,7 +356,7 @@ h3a_status h3a_rope_plan_from(int32_t rotary_dim, int32_t interleaved, const dou
  * Errors: INVALID_ARG for null or misaligned pointers, tokens < 0, heads < 1,
  * head_dim < rotary_dim, head_dim or a stride no multiple of 8, a stride
  * smaller than what it steps over or a plan not made by the calls above;
- * UNSUPPORTED for head_dim > 512, tokens >= 2^31 or more than 65,535 heads in
+ * UNSUPPORTED for head_dim > 512, tokens >= 2^31 or more than 32,768 heads in
  * all. */
 h3a_status h3a_rope(const void* q, void* q_out, const h3a_heads_desc* dq, const void* k, void* k_out,
                     const h3a_heads_desc* dk, h3a_dtype dtype, const int32_t* positions, int64_t tokens,
@@ -399,8 +404,12 @@ typedef struct {
 } h3a_packed_desc;
 
 /* Bytes of device workspace h3a_packed_attention needs for this descriptor: 0
- * when no sequence's keys are split, else one fp32 partial row and its
- * log-sum-exp per (split, query, head). */
+ * when no sequence's keys are cut into parts, else the parts' fp32 rows and
+ * log-sum-exps (a few MB for single tokens over caches; for prompts and pieces
+ * of them, one row for each part, query and head).  It goes by the descriptor
+ * alone, so a workspace for the largest shapes of a program serves the whole
+ * range only if it is asked for each of them.  Errors: those of
+ * h3a_packed_attention that concern the descriptor. */
 h3a_status h3a_packed_attention_workspace_size(const h3a_packed_desc* d, size_t* bytes);
 
 /* Attention over packed sequences with grouped heads, causal or not: whole
@@ -420,11 +429,13 @@ h3a_status h3a_packed_attention_workspace_size(const h3a_packed_desc* d, size_t*
  * int32 [seqs] or NULL.  Values that do not fit total_q / total_k are cut to
  * them (no access outside the tensors).
  * max_q bounds the sequences' queries (rows past it are left as they were);
- * max_k only sizes the splits, so a wrong one costs time, not correctness.
+ * max_k only decides how keys are cut into parts, so a wrong one costs time, not
+ * correctness.
  * lse       : device fp32 [total_q, heads], contiguous, or NULL.
  * workspace : device, h3a_packed_attention_workspace_size bytes, 16-byte
- *             aligned; NULL when that is 0.  Calls that may overlap on the GPU
- *             need workspaces of their own.
+ *             aligned; NULL when that is 0.  It needs no preparation and holds
+ *             nothing from call to call; calls that may overlap on the GPU
+ *             (captured ones too) need workspaces of their own.
  * QK^T and PV run on the tensor cores with fp32 accumulation; logits, maxima
  * and sums are fp32; P is rounded to the element type for PV; o is rounded
  * once.
@@ -432,8 +443,11 @@ h3a_status h3a_packed_attention_workspace_size(const h3a_packed_desc* d, size_t*
  * positive multiple of kv_heads, negative sizes, max_q or max_k < 0, a stride no
  * multiple of 8 or smaller than what it steps over, an unknown dtype, a scale
  * that is negative or not finite; UNSUPPORTED for head_dim other than 64 / 96 /
- * 128, more than 128 heads to a kv head, total_q or total_k >= 2^31, or a grid
- * beyond 2^31 blocks; WORKSPACE if it is null, misaligned or too small. */
+ * 128, more than 128 heads to a kv head, total_q, total_k or total_q * heads
+ * >= 2^31, strides of 2^39 elements, or a grid beyond 2^31 blocks (65,535 kv heads
+ * for more than 16 rows, queries x heads, a kv head); WORKSPACE if it is null,
+ * misaligned or too small.  A bounded device-side wait that expired is reported by
+ * h3a_last_device_error. */
 h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, const h3a_packed_desc* d,
                                 const int32_t* starts_q, const int32_t* starts_k, const int32_t* lengths_k, void* o,
                                 float* lse, void* workspace, size_t ws_bytes, h3a_stream_t stream);

@@ -526,7 +526,7 @@ h3a_status h3a_rope(const void* q, void* q_out, const h3a_heads_desc* dq, const 
         side[i] = RopeSide{x, y, d.stride_n, d.stride_h, d.out_stride_n, d.out_stride_h, d.heads};
         heads += d.heads;
     }
-    if (dq->head_dim > 512 || tokens >= (int64_t(1) << 31) || heads > 65535) return H3A_ERR_UNSUPPORTED;
+    if (dq->head_dim > 512 || tokens >= (int64_t(1) << 31) || heads > 32768) return H3A_ERR_UNSUPPORTED;
     if (tokens == 0) return H3A_OK;
     if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u)) return H3A_ERR_INVALID_ARG;
     cudaError_t e = launch_rope(side[0], side[1], dq->head_dim, dtype == H3A_FP16, positions, tokens, *plan, inverse != 0,

@@ -140,6 +140,55 @@ def test_nonfinite_where_not_attended(lq, cached, group, d):
     assert o[last].isnan().all()
 
 
+@pytest.mark.parametrize("lq,cached,heads,kv", [([3, 1, 4], [9000, 40, 700], 8, 2), ([130], [9000], 2, 2)], ids=str)
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_nonfinite_where_not_attended_in_parts(lq, cached, heads, kv, d):
+    """The same with keys cut into parts: infinities near the diagonal, NaN in the middle for everyone."""
+    lk = [a + b for a, b in zip(lq, cached)]
+    q, k, v = make(lq, lk, heads, kv, d, seed=6)
+    v[lk[0] - 1, 0, 5] = -math.inf
+    v[lk[0] - 2, kv - 1, d - 2] = math.nan
+    v[4321, 0, 9] = math.inf
+    check(q, k, v, starts(lq), starts(lk))
+
+
+@pytest.mark.parametrize("lk", [[30, 40], [9000, 500]], ids=str)
+@pytest.mark.parametrize("most", [1, 2, 5, 40])
+def test_rows_past_max_q_are_left(lk, most):
+    """max_q smaller than the sequences: the rows up to it are right, the others as they were."""
+    lq = [50, 3] if most == 40 else [7, 3]
+    q, k, v = make(lq, lk, 4, 2, 64)
+    out = torch.full_like(q, 3.0)
+    o, lse = h3a.packed_attention(q, k, v, dev(starts(lq)), dev(starts(lk)), most, max(lk), out=out, return_lse=True)
+    want, want_lse, bound, lse_bound = ref.attention(q, k, v, starts(lq), starts(lk))
+    for a, n in zip(starts(lq), lq):
+        m = min(n, most)
+        ref.within(o[a:a + m], want[a:a + m], bound[a:a + m])
+        ref.within(lse[a:a + m], want_lse[a:a + m], lse_bound[a:a + m])
+        assert (o[a + m:a + n] == 3.0).all()
+
+
+@pytest.mark.parametrize("lq", [1, 20])
+def test_many_sequences(lq):
+    """More sequences than are tried or counted at once, most of them short, some empty."""
+    rng = random.Random(lq)
+    n = 1300
+    lk = [rng.choice([0, 1, 5, 17, 30]) + (lq if lq > 1 else 0) for _ in range(n)]
+    lk[777] = 6000
+    lqs = [rng.choice([0, lq, 1]) for _ in range(n)]
+    q, k, v = make(lqs, lk, 4, 2, 64, seed=3)
+    check(q, k, v, starts(lqs), starts(lk))
+    check(q, k, v, starts(lqs), starts(lk), causal=False)
+
+
+@pytest.mark.parametrize("kv,heads", [(3, 3), (28, 28), (64, 128), (300, 300), (1, 16)])
+def test_streamed_heads(kv, heads):
+    """Long caches with numbers of kv heads that do and do not divide the GPU."""
+    lk = [3000, 1, 64, 2500]
+    q, k, v = make([1] * 4, lk, heads, kv, 64, seed=8)
+    check(q, k, v, starts([1] * 4), starts(lk))
+
+
 def test_neighbours_are_not_touched():
     """Sequences of NaN around one of numbers, and tensors whose rows go on behind the last sequence."""
     lq = [60, 70, 50]
