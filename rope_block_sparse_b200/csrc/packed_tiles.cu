@@ -204,33 +204,47 @@ __device__ __forceinline__ bool find_work(const TileArgs& a, int tiles, Work& w)
     return w.split == 0 || w.steps() > 0;
 }
 
+// The loads of one step of K or V into buffer `stage`.
 template <class G>
-__device__ void producer(Smem<G>& sm, const TileArgs& a, const Work& w, const CUtensorMap* tq, const CUtensorMap* tk,
-                         const CUtensorMap* tv, volatile int* abort_flag) {
-    const uint32_t q_bytes = G::kChunks * 64u * static_cast<uint32_t>(a.per_tile * a.p.group);
-    const int q0 = static_cast<int>(w.s.q0) + w.t0, k0 = static_cast<int>(w.s.k0) + w.begin, kvh = w.kvh;
-    auto load_q = [&](int t) {
-        mbar_arrive_expect_tx(&sm.q_full[t], q_bytes);
-        for (int c = 0; c < G::kChunks; ++c)
-            tma_load_4d(sm.q[t] + c * kChunkBytes, tq, &sm.q_full[t], 32 * c, 0, kvh, q0 + t * a.per_tile);
-    };
-    // a tile without steps needs no Q (its rows' zeros go out through that memory)
-    if (w.n0 > 0) load_q(0);
+__device__ __forceinline__ void load_kv(uint8_t* tile, const CUtensorMap* map, uint64_t* full, const Work& w, int j) {
+    mbar_arrive_expect_tx(full, G::kTileBytes);
+    const int row = static_cast<int>(w.s.k0) + w.begin + j * 128;
+    for (int c = 0; c < G::kChunks; ++c) tma_load_4d(tile + c * kChunkBytes, map, full, 32 * c, w.kvh, row, 0);
+}
+
+template <class G>
+__device__ __forceinline__ void load_q(Smem<G>& sm, const TileArgs& a, const CUtensorMap* map, const Work& w, int t) {
+    mbar_arrive_expect_tx(&sm.q_full[t], G::kChunks * 64u * static_cast<uint32_t>(a.per_tile * a.p.group));
+    const int row = static_cast<int>(w.s.q0) + w.t0 + t * a.per_tile;
+    for (int c = 0; c < G::kChunks; ++c) tma_load_4d(sm.q[t] + c * kChunkBytes, map, &sm.q_full[t], 32 * c, 0, w.kvh, row);
+}
+
+// The first loads, before the CTA's other warps are ready: the first K behind the
+// first Q, since the first MMA waits for these two.  A tile without steps needs no
+// Q (its rows' zeros go out through that memory).
+template <class G>
+__device__ __forceinline__ void load_first(Smem<G>& sm, const TileArgs& a, const Work& w, const CUtensorMap* tq, const CUtensorMap* tk,
+                                           const CUtensorMap* tv) {
+    if (w.n0 > 0) load_q(sm, a, tq, w, 0);
+    if (w.steps() == 0) return;
+    load_kv<G>(sm.k[0], tk, &sm.k_full[0], w, 0);
+    if (w.n1 > 0) load_q(sm, a, tq, w, G::kTiles - 1);
+    load_kv<G>(sm.v[0], tv, &sm.v_full[0], w, 0);
+}
+
+template <class G>
+__device__ void producer(Smem<G>& sm, const TileArgs& a, const Work& w, const CUtensorMap* tk, const CUtensorMap* tv,
+                         volatile int* abort_flag) {
     const int n = w.steps();
-    uint32_t stage = 0, phase = 0;
     bool ok = true;
-    int issued_k = 0, issued_v = 0;
-    for (int j = 0; j < n; ++j) {
+    int issued_k = min(n, 1), issued_v = issued_k;
+    uint32_t stage = G::kStages > 1 ? 1 : 0, phase = G::kStages > 1 ? 0 : 1;
+    for (int j = 1; j < n; ++j) {
         if (!(ok = mbar_wait(&sm.k_empty[stage], phase ^ 1u, abort_flag, a.timeout_ns))) break;
-        mbar_arrive_expect_tx(&sm.k_full[stage], G::kTileBytes);
-        for (int c = 0; c < G::kChunks; ++c)
-            tma_load_4d(sm.k[stage] + c * kChunkBytes, tk, &sm.k_full[stage], 32 * c, kvh, k0 + j * 128, 0);
+        load_kv<G>(sm.k[stage], tk, &sm.k_full[stage], w, j);
         ++issued_k;
-        if (j == 0 && w.n1 > 0) load_q(1);  // behind the K that the first tile waits for
         if (!(ok = mbar_wait(&sm.v_empty[stage], phase ^ 1u, abort_flag, a.timeout_ns))) break;
-        mbar_arrive_expect_tx(&sm.v_full[stage], G::kTileBytes);
-        for (int c = 0; c < G::kChunks; ++c)
-            tma_load_4d(sm.v[stage] + c * kChunkBytes, tv, &sm.v_full[stage], 32 * c, kvh, k0 + j * 128, 0);
+        load_kv<G>(sm.v[stage], tv, &sm.v_full[stage], w, j);
         ++issued_v;
         if (++stage == G::kStages) {
             stage = 0;
@@ -241,7 +255,7 @@ __device__ void producer(Smem<G>& sm, const TileArgs& a, const Work& w, const CU
     // Drain: every load issued must have landed before the CTA may exit.
     volatile int* never = &sm.never;
     if (w.n0 > 0) mbar_wait(&sm.q_full[0], 0u, never, a.timeout_ns);
-    if (issued_k > 0 && w.n1 > 0) mbar_wait(&sm.q_full[1], 0u, never, a.timeout_ns);
+    if (w.n1 > 0) mbar_wait(&sm.q_full[1], 0u, never, a.timeout_ns);
     for (int i = max(0, issued_k - G::kStages); i < issued_k; ++i)
         mbar_wait(&sm.k_full[i % G::kStages], (i / G::kStages) & 1u, never, a.timeout_ns);
     for (int i = max(0, issued_v - G::kStages); i < issued_v; ++i)
@@ -652,62 +666,93 @@ __device__ void softmax_group(Smem<G>& sm, const TileArgs& a, const Work& w, uin
     const int64_t tok = w.s.q0 + query, qh = tok * a.p.heads + head;
     const bool split = a.p.splits > 1;
     // A warp's 32 rows go out through the Q tile's shared memory (no MMA reads
-    // it any more), 64 or 128 bytes of each at a time, so that a warp writes whole
-    // pieces of rows: a thread's own row would be written 16 bytes here and 16
-    // there.  16-byte pieces are swizzled by the row so that neither side collides.
+    // it any more), 64 bytes of each at a time, four lanes a row: a thread's own row
+    // would be written 16 bytes here and 16 there.  16-byte pieces are swizzled by
+    // the row so that neither side collides.
     const int64_t rows = a.p.total_q * a.p.heads;
     int64_t* places = sm.place[t * 4 + quarter];
     places[lane] = !there ? -1 : split ? (w.split * rows + qh) * D : tok * a.p.on + head * a.p.oh;
-    uint4* stage = reinterpret_cast<uint4*>(sm.q[t]) + quarter * 32 * (D / 8);
     __syncwarp();
-    const bool keys = n > 0 && l != 0.f;
-#pragma unroll 1
-    for (int cc = 0; cc < G::kChunks; ++cc) {
-        uint32_t x[32];
+    int64_t at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[i] = places[i * 8 + lane / 4];
+    uint4* stage = reinterpret_cast<uint4*>(sm.q[t]) + quarter * 32 * (D / 8);
+    const int mine = lane * 4, turn = (lane >> 1) & 3;
+    auto theirs = [&](int i) { return (i * 8 + lane / 4) * 4 + ((lane & 3) ^ ((lane >> 3) & 3)); };
+    // what warp 11 cleared, for a row that attends it
+    auto restore = [&](uint32_t* x, int channel) {
+        float tmp[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) tmp[i] = __uint_as_float(x[i]);
+        add_nonfinite<FP16>(tmp, static_cast<const uint16_t*>(a.p.v) + w.s.k0 * a.p.vn + w.kvh * a.p.vh + channel, a.p.vn,
+                            w.begin + 128 * w.clean, limit_of(query));
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(tmp[i]);
+    };
+    if (!split) {
+        uint32_t x[D];
         if (n > 0) {
-            tmem_ld_x32(tO + 32u * cc, x);
-            tmem_wait_ld_x32(x);
-        }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = keys ? __float_as_uint(__uint_as_float(x[i]) * inv_l) : 0u;
-        if (cleared && there) {
-            float tmp[32];
+            for (int cc = 0; cc < G::kChunks; ++cc) tmem_ld_x32(tO + 32u * cc, slice32(x + 32 * cc));
 #pragma unroll
-            for (int i = 0; i < 32; ++i) tmp[i] = __uint_as_float(x[i]);
-            add_nonfinite<FP16>(tmp, static_cast<const uint16_t*>(a.p.v) + w.s.k0 * a.p.vn + w.kvh * a.p.vh + 32 * cc, a.p.vn,
-                                w.begin + 128 * w.clean, limit_of(query));
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(tmp[i]);
-        }
-        if (split) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                stage[lane * 8 + (i ^ (lane & 7))] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = i * 4 + lane / 8, piece = lane & 7;
-                const uint4 v = stage[r * 8 + (piece ^ (r & 7))];
-                const int64_t at = places[r];
-                if (at >= 0) reinterpret_cast<uint4*>(a.p.part_o + at + 32 * cc)[piece] = v;
-            }
+            for (int cc = 0; cc < G::kChunks; ++cc) tmem_wait_ld_x32(slice32(x + 32 * cc));
         } else {
-            uint32_t h[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) h[i] = H::pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            for (int i = 0; i < D; ++i) x[i] = 0;
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-            __syncwarp();
+        for (int cc = 0; cc < G::kChunks; ++cc) {
+#pragma unroll
+            for (int i = 32 * cc; i < 32 * cc + 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * inv_l);
+            if (cleared && there) restore(x + 32 * cc, 32 * cc);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = i * 8 + lane / 4, piece = lane & 3;
-                const uint4 v = stage[r * 4 + (piece ^ ((r >> 1) & 3))];
-                const int64_t at = places[r];
-                if (at >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.p.o) + at + 32 * cc)[piece] = v;
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    h[e] = H::pack(__uint_as_float(x[32 * cc + 8 * i + 2 * e]), __uint_as_float(x[32 * cc + 8 * i + 2 * e + 1]));
+                stage[128 * cc + mine + (i ^ turn)] = make_uint4(h[0], h[1], h[2], h[3]);
             }
         }
         __syncwarp();
+#pragma unroll
+        for (int cc = 0; cc < G::kChunks; ++cc)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = stage[128 * cc + theirs(i)];
+                if (at[i] >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.p.o) + at[i] + 32 * cc)[lane & 3] = v;
+            }
+    } else {
+#pragma unroll 1
+        for (int cc = 0; cc < G::kChunks; ++cc) {
+            uint32_t x[32];
+            if (n > 0) {
+                tmem_ld_x32(tO + 32u * cc, x);
+                tmem_wait_ld_x32(x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * inv_l);
+            if (cleared && there) restore(x, 32 * cc);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    stage[128 * h + mine + (i ^ turn)] =
+                        make_uint4(x[16 * h + 4 * i], x[16 * h + 4 * i + 1], x[16 * h + 4 * i + 2], x[16 * h + 4 * i + 3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 v = stage[128 * h + theirs(i)];
+                    if (at[i] >= 0) reinterpret_cast<uint4*>(a.p.part_o + at[i] + 32 * cc + 16 * h)[lane & 3] = v;
+                }
+            __syncwarp();
+        }
     }
     if (there) {
         if (split)
@@ -726,25 +771,38 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
     Smem<G>& sm = *reinterpret_cast<Smem<G>*>(smem_raw + (((base + 1023u) & ~1023u) - base));
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel, if there is one, may be set up
     const int warp = threadIdx.x >> 5;
-    if (warp == G::kMmaWarp) {
+    if (warp == G::kProducerWarp) {
+        // the work and its first loads, while the other warps set up the rest
+        if ((threadIdx.x & 31) == 0) {
+            prefetch_tensor_map(&tq);
+            prefetch_tensor_map(&tk);
+            prefetch_tensor_map(&tv);
+            for (int t = 0; t < 2; ++t) mbar_init(&sm.q_full[t], 1);
+            for (int s = 0; s < G::kStages; ++s) {
+                mbar_init(&sm.k_full[s], 1);
+                mbar_init(&sm.k_empty[s], 1);
+                mbar_init(&sm.v_full[s], 1);
+                mbar_init(&sm.v_ready[s], 1);
+                mbar_init(&sm.v_empty[s], 1);
+            }
+            fence_barrier_init();
+        }
+        Work mine;
+        mine.none = !find_work(a, G::kTiles, mine);
+        if ((threadIdx.x & 31) == 0) {
+            if (!mine.none) load_first<G>(sm, a, mine, &tq, &tk, &tv);
+            sm.work = mine;
+        }
+    } else if (warp == G::kMmaWarp) {
         tmem_alloc(&sm.tmem_base, G::kTmemCols);
         tmem_relinquish();
-    }
-    if (threadIdx.x == 0) {
+    } else if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&sm.q_full[t], 1);
             mbar_init(&sm.s_full[t], 1);
             mbar_init(&sm.p_full[t], 4);  // one arrival per softmax warp of the tile
             mbar_init(&sm.o_done[t], 1);
             mbar_init(&sm.s_read[t], 4);
             mbar_init(&sm.pv_done[t], 1);
-        }
-        for (int s = 0; s < G::kStages; ++s) {
-            mbar_init(&sm.k_full[s], 1);
-            mbar_init(&sm.k_empty[s], 1);
-            mbar_init(&sm.v_full[s], 1);
-            mbar_init(&sm.v_ready[s], 1);
-            mbar_init(&sm.v_empty[s], 1);
         }
         mbar_init(&sm.mma_drain, 1);
         mbar_init(&sm.pv_drain, 1);
@@ -753,16 +811,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
         sm.nonfinite = 0;
         fence_barrier_init();
     }
-    if (warp == G::kProducerWarp && (threadIdx.x & 31) == 0) {
-        prefetch_tensor_map(&tq);
-        prefetch_tensor_map(&tk);
-        prefetch_tensor_map(&tv);
-    }
-    {
-        Work mine;
-        mine.none = !find_work(a, G::kTiles, mine);
-        if (threadIdx.x == 0) sm.work = mine;
-    }
+    __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -780,7 +829,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kRegsOther));
         const bool one = (threadIdx.x & 31) == 0;
         if (warp == G::kProducerWarp) {
-            if (one) producer<G>(sm, a, w, &tq, &tk, &tv, abort_flag);
+            if (one) producer<G>(sm, a, w, &tk, &tv, abort_flag);
         } else if (warp == G::kMmaWarp) {
             if (one) {
                 if constexpr (G::kSepP)
