@@ -64,7 +64,7 @@ def _binding_cmd(out: str) -> list:
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-I", INCLUDE, *[x for i in includes for x in ("-isystem", i)], os.path.join(CSRC, "binding.cpp"), "-o", out,
             "-L", libs, "-L", PKG, "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}", "-l:libh3a.so", "-lc10", "-lc10_cuda", "-ltorch_cpu",
-            "-ltorch_python"]
+            "-ltorch_cuda", "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

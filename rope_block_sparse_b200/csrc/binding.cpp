@@ -5,7 +5,7 @@
 // four.  Every function is positional and returns new or given tensors; wrong
 // arguments raise ValueError, a status other than H3A_OK the H3AError of h3a.py.
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -69,7 +69,7 @@ const int32_t* check_index(const at::Tensor& t, const char* name, int64_t n, con
 }
 
 at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& like) {
-    return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
+    return at::Tensor(at::detail::empty_cuda(sizes, type, like.device(), std::nullopt));
 }
 
 h3a_stream_t stream_of(const at::Tensor& t) {

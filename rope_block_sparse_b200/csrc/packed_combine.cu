@@ -22,8 +22,7 @@ __global__ void __launch_bounds__(kThreads) packed_combine_kernel(const __grid_c
     __shared__ float joined[WARPS][D];
     __shared__ float joined_top[WARPS], joined_sum[WARPS];
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS, row = (threadIdx.x >> 5) / WARPS;
-    // launched while the parts are still computed (run): wait for them
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    early_start();
     const int64_t qh = static_cast<int64_t>(blockIdx.x) * kRows + row;
     const int64_t n = qh / a.heads;
     const int head = static_cast<int>(qh - n * a.heads);
@@ -136,18 +135,7 @@ __global__ void __launch_bounds__(kThreads) packed_combine_kernel(const __grid_c
 template <int D, bool FP16, int WARPS>
 cudaError_t run(const PackedArgs& a, cudaStream_t st) {
     const int64_t rows = a.total_q * a.heads, per = kThreads / 32 / WARPS;
-    // Programmatic dependent launch: this kernel's CTAs are set up while the last
-    // parts are computed.
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per));
-    c.blockDim = dim3(kThreads);
-    c.stream = st;
-    c.attrs = &early;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, packed_combine_kernel<D, FP16, WARPS>, a);
+    return launch_early(packed_combine_kernel<D, FP16, WARPS>, dim3(static_cast<unsigned>((rows + per - 1) / per)), kThreads, 0, st, a);
 }
 
 template <int D>

@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(32 * W, W == kWarps ? packed_rows_ctas(D) : 1)
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int found[2];
     if (threadIdx.x == 0) found[0] = found[1] = 0;
+    early_start();
     __syncthreads();
     const PackedSeq s = packed_seq(a, blockIdx.x / a.kv_heads);
     const int queries = counted_queries(a, s);
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(32 * kWarps, packed_rows_ctas(D)) packed_strea
     __shared__ int64_t sums[kWarps];
     __shared__ int64_t start_blocks;  // blocks before the sequence the stretch starts in
     __shared__ int start_seq;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may be set up
+    early_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // Blocks of all sequences: each thread counts a run of them, then a scan.
     const int run = (a.seqs + (32 * kWarps) - 1) / (32 * kWarps);
@@ -428,8 +429,7 @@ cudaError_t launch(const PackedArgs& a, cudaStream_t st) {
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
     if (e != cudaSuccess) return e;
     const int64_t grid = static_cast<int64_t>(STREAM ? a.streams : a.seqs) * a.kv_heads;
-    kernel<<<static_cast<unsigned>(grid), 32 * W, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3(static_cast<unsigned>(grid)), 32 * W, smem, st, a);
 }
 
 template <int D, bool FP16>

@@ -769,7 +769,6 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     Smem<G>& sm = *reinterpret_cast<Smem<G>*>(smem_raw + (((base + 1023u) & ~1023u) - base));
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel, if there is one, may be set up
     const int warp = threadIdx.x >> 5;
     if (warp == G::kProducerWarp) {
         // the work and its first loads, while the other warps set up the rest
@@ -787,6 +786,8 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
             }
             fence_barrier_init();
         }
+        __syncwarp();
+        early_start();
         Work mine;
         mine.none = !find_work(a, G::kTiles, mine);
         if ((threadIdx.x & 31) == 0) {
@@ -812,6 +813,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
         fence_barrier_init();
     }
     __syncwarp();
+    if (warp != G::kProducerWarp) early_start();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -860,8 +862,7 @@ cudaError_t run(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap&
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(packed_tiles_kernel<G, FP16>), static_cast<int>(smem), done);
     if (e != cudaSuccess) return e;
     const dim3 grid(a.pairs, a.p.kv_heads, a.p.splits);
-    packed_tiles_kernel<G, FP16><<<grid, G::kThreads, smem, st>>>(tq, tk, tv, a);
-    return cudaGetLastError();
+    return launch_early(packed_tiles_kernel<G, FP16>, grid, G::kThreads, smem, st, tq, tk, tv, a);
 }
 
 template <int TILES>

@@ -19,6 +19,30 @@ constexpr int kSms = 148;  // B200
 // (`done`: a bit for each device, of its own for each kernel).
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
+// Programmatic dependent launch.  The prompt side's kernels are launched with
+// launch_early and call early_start before they touch global memory: their CTAs
+// may then be set up while the stream's kernel before them still runs, and begin
+// the moment it is complete and its writes are visible.  They let the kernel
+// after them do the same as soon as all their own CTAs have started.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+__device__ __forceinline__ void early_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // One-dimensional rotary positions (rope.cu).  A side with heads == 0 is absent.
 struct RopeSide {
     const void* x;

@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(LANES ? 128 : 512) residual_rmsnorm_kernel(con
         }
         if (kRing) asm volatile("cp.async.commit_group;" ::: "memory");  // an empty group keeps the count
     };
+    early_start();
 #pragma unroll
     for (int i = 0; i < (kRing ? kStages - 1 : 1); ++i) fetch(row + i * rows_at_once, i);
     float g[VPT][8];
@@ -222,8 +223,7 @@ cudaError_t launch(const RmsNormArgs& a, int threads, cudaStream_t st) {
     const int per_sm = std::max(1, ring ? std::min(2048 / threads, (200 << 10) / smem) : 1024 / threads);
     const int64_t rows = LANES ? threads / LANES : 1;
     const int64_t grid = std::min<int64_t>((a.rows + rows - 1) / rows, kSms * per_sm);
-    residual_rmsnorm_kernel<VPT, LANES, FP16, SCALES, RES><<<static_cast<unsigned>(grid), threads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(residual_rmsnorm_kernel<VPT, LANES, FP16, SCALES, RES>, dim3(static_cast<unsigned>(grid)), threads, smem, st, a);
 }
 
 template <int VPT, int LANES, bool FP16>

@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     for (int i = threadIdx.x; i < pairs; i += kThreads)
         asm volatile("ld.u64 %0, [%1];" : "=l"(turns[i]) : "l"(&a.plan.turns[i]));
 
+    early_start();
+
     const int slot = threadIdx.x % a.slots;
     const int group = threadIdx.x / a.slots;
     const bool busy = group < a.groups, turn = slot < rotated;
@@ -238,8 +240,7 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t st) {
     const size_t tokens = (per_chunk + a.heads - 2) / a.heads + 1;  // that a chunk may touch
     // at most 35 KB of angles and 8 KB of heads
     const size_t smem = tokens * row * sizeof(float2) + (MODE == kHalvesAny ? static_cast<size_t>(per_chunk) * rotated * 16 : 0);
-    rope_kernel<FP16, MODE, ITEMS><<<static_cast<unsigned>(chunks < most ? chunks : most), kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(rope_kernel<FP16, MODE, ITEMS>, dim3(static_cast<unsigned>(chunks < most ? chunks : most)), kThreads, smem, st, a);
 }
 
 template <bool FP16, Mode MODE>
