@@ -6,9 +6,6 @@
 
 #include "prompt_internal.h"
 
-#ifndef ONE_TILE_KEYS
-#define ONE_TILE_KEYS -1
-#endif
 namespace h3a {
 
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
@@ -50,10 +47,10 @@ int64_t tile_splits(const h3a_packed_desc& d, int tiles, int64_t max_q, int64_t 
     double least = 0;
     for (int64_t s = 1; s <= 64 && (s == 1 || steps / s >= 2); ++s) {
         const double longest = std::ceil(steps / s) + 4, waves = base * s / slots;
-        const double units = waves <= 1 ? longest : std::max(longest, waves * (mean / s + 4) + 0.5 * longest);
+        const double units = waves <= 1 ? longest : std::max(longest, waves * (mean / s + 4) + 0.25 * longest);
         const double us = units * step_us + (s > 1 ? 4 + rows_us * s : 0);
         // a clear gain only: the lengths are guessed, and tiles come in whole numbers
-        if (s == 1 || us < (best == 1 ? 0.75 : 0.95) * least) {
+        if (s == 1 || us < (best == 1 ? 0.75 : 0.97) * least) {
             best = s;
             least = us;
         }
