@@ -17,8 +17,8 @@
 // 4,096 with it 39.7 and 42.)  The sum of squares and max|h * gamma| are reduced
 // together (one barrier a row, none for parts of a warp); max|y| is r times the
 // latter.  Divisions are taken once a row or group, as reciprocals.
-// Measured: 124,992 rows of 5,376 with residual and row scales 776 us (4.70 GB,
-// 6.06 TB/s = 0.92 of a copy), 8,192 of 4,096 with group scales 39.7 us (0.91).
+// Measured: 124,992 rows of 5,376 with residual and row scales 784 us (4.70 GB,
+// 6.0 TB/s = 0.91 of a copy), 8,192 of 4,096 with group scales 40.6 us (0.89).
 #include <algorithm>
 
 #include "half16.cuh"
@@ -172,10 +172,12 @@ __global__ void __launch_bounds__(LANES ? 128 : 512) residual_rmsnorm_kernel(con
             if (SCALES == H3A_SCALES_ROW) most = __shfl_sync(0xffffffffu, most, 0);
         }
         const float r = rsqrtf(fmaf(sum, inv_width, a.eps));
-        float q = r;  // what turns h * gamma into what is rounded
+        // What turns y = h * gamma * r into what is rounded.  Not multiplied into r: with
+        // small rows (r large) and a group of zeros (scale least) their product overflows.
+        float q = 1.f;
         if (SCALES == H3A_SCALES_ROW) {
             const float scale = max_nan(most * r, kLeastAmax) * (1.0f / kE4m3Most);
-            q = r * __frcp_rn(scale);
+            q = __frcp_rn(scale);
             if (there && mine == 0) a.scales[row] = scale;
         }
 #pragma unroll
@@ -187,16 +189,18 @@ __global__ void __launch_bounds__(LANES ? 128 : 512) residual_rmsnorm_kernel(con
 #pragma unroll
                 for (int o = LANES && LANES < 16 ? LANES / 2 : 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                 const float scale = max_nan(m * r, kLeastAmax) * (1.0f / kE4m3Most);
-                q = r * __frcp_rn(scale);
+                q = __frcp_rn(scale);
                 if (there && v < nvec && (v & 15) == 0) a.scales[row * ((nvec + 15) / 16) + v / 16] = scale;
             }
             if (!there || v >= nvec) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[u][i] *= r;
             if (SCALES == H3A_SCALES_NONE) {
                 uint4 w;
-                w.x = H::pack(y[u][0] * q, y[u][1] * q);
-                w.y = H::pack(y[u][2] * q, y[u][3] * q);
-                w.z = H::pack(y[u][4] * q, y[u][5] * q);
-                w.w = H::pack(y[u][6] * q, y[u][7] * q);
+                w.x = H::pack(y[u][0], y[u][1]);
+                w.y = H::pack(y[u][2], y[u][3]);
+                w.z = H::pack(y[u][4], y[u][5]);
+                w.w = H::pack(y[u][6], y[u][7]);
                 reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + row * a.ys)[v] = w;
             } else {
                 uint2 w;

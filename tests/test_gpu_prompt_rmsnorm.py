@@ -102,6 +102,28 @@ def test_rmsnorm_zero_and_nonfinite_rows(scales):
         assert y[3, 5].isnan() and not y[3, 6:].any()
 
 
+@pytest.mark.parametrize("width", [256, 1024, 4096])
+@pytest.mark.parametrize("scales", [None, "row", "group"])
+def test_rmsnorm_small_rows_without_eps(width, scales):
+    """Rows of about 1e-12 and no eps: 1 / rms is 1e12, and the reciprocal of the least scale 448 * 2^100.  Channels
+    that are zero (a group of them, or by gamma) stay zero."""
+    x, _, gamma = draw(3, width, seed=9)
+    x = (x.float() * 1e-12).to(x.dtype)
+    x[1, 128:256] = 0
+    _, want = ref.rmsnorm(x, None, gamma, 0.0)
+    _, y, s = h3a.residual_rmsnorm(x, None, gamma, 0.0, scales=scales)
+    got = y.double()
+    if scales:
+        got = got * (s[:, None] if scales == "row" else s.repeat_interleave(128, 1)).double()
+    amax = want.abs().view(3, -1, width if scales == "row" else 128).amax(2, keepdim=True).expand(-1, -1, width if scales == "row" else 128)
+    half = 2.0 ** -4 if scales else ref.half_step(x.dtype)
+    # e4m3: half a step relative, and half a step of its subnormals, 2^-10 scales of amax / 448
+    ref.within(got, want, want.abs() * (half + 8 * ref.RMSNORM_RELATIVE) + (amax.reshape(want.shape) / 448 * 2.0 ** -10 * 1.01 if scales else 0), "small")
+    assert not y[1, 128:256].float().any()
+    _, y, s = h3a.residual_rmsnorm(x, None, torch.zeros_like(gamma), 0.0, scales=scales)
+    assert not y.float().any() and (s is None or torch.equal(s, torch.full_like(s, 2.0 ** -100 / 448)))
+
+
 def test_rmsnorm_is_deterministic_and_row_wise():
     """A row's result does not depend on its place or on the rows around it."""
     x, f, gamma = draw(3000, 512, seed=6)
