@@ -52,6 +52,8 @@ h3a_dtype check_rows(const at::Tensor& t, const char* name, int dims) {
     require(t.is_cuda(), name, "must be on a CUDA device (libh3a has no CPU path)");
     if (t.dim() != dims || (t.stride(dims - 1) != 1 && t.size(dims - 1) > 1))
         throw Refused{std::string(name) + " must have " + std::to_string(dims) + " dimensions, the last one contiguous"};
+    // the descriptors hold them in 32 bits
+    for (int i = 1; i < dims; ++i) require(t.size(i) <= INT32_MAX, name, "has a dimension of 2^31 or more");
     return type == at::kHalf ? H3A_FP16 : H3A_BF16;
 }
 

@@ -437,7 +437,7 @@ def rope_plan(rotary_dim: int, theta: float = 10000.0, interleaved: bool = False
     """Rotary frequencies for rope(): theta^(-2j/rotary_dim), stretched for long contexts by `scaling`
     ("none", "linear", "base", "parts": see h3a_rope_scaling), or the given `frequencies` (radians per
     position, rotary_dim / 2 numbers).  interleaved: pairs (2j, 2j+1), else (j, j + rotary_dim/2).
-    Host only; plans of the same arguments are made once."""
+    Host only; plans of the same arguments are made once and shared, so they are not to be written to."""
     if scaling not in _ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
     return _rope_plan(int(rotary_dim), float(theta), bool(interleaved), scaling, float(factor), int(original_length),
@@ -487,6 +487,8 @@ def residual_rmsnorm(x: torch.Tensor, f: torch.Tensor | None, gamma: torch.Tenso
 
 def packed_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, seqs: int, max_q: int, max_k: int) -> int:
     """Bytes of workspace packed_attention() needs for these shapes (0: none)."""
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
     n = ctypes.c_size_t(0)
     d = PackedDesc(_DTYPES[q.dtype], seqs, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], max_q, max_k,
                    *q.stride()[:2], *k.stride()[:2], *k.stride()[:2], *q.stride()[:2], 1, 0.0)

@@ -148,3 +148,9 @@ def test_rmsnorm_empty_and_refusals():
         h3a.residual_rmsnorm(z, None, torch.ones(16392, device="cuda"))
     with pytest.raises(h3a.H3AError, match="INVALID_ARG"):
         h3a.residual_rmsnorm(x[:, :60].contiguous(), None, gamma[:60].contiguous())
+
+
+def test_rmsnorm_refuses_widths_past_32_bits():
+    x = torch.empty(1, 2 ** 31 + 8, device="cuda", dtype=torch.bfloat16)  # 4.3 GB, not touched
+    with pytest.raises(ValueError, match="2\\^31"):
+        h3a.residual_rmsnorm(x, None, torch.ones(8, device="cuda"))
