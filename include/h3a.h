@@ -425,12 +425,14 @@ h3a_status h3a_packed_attention_workspace_size(const h3a_packed_desc* d, size_t*
  * lse = -inf.  What a query does not attend has no influence on it, NaN and
  * infinities included.  Rows of o and lse outside every sequence are left as
  * they were.
- * starts_q, starts_k: device int32 [seqs + 1], ascending; lengths_k: device
- * int32 [seqs] or NULL.  Values that do not fit total_q / total_k are cut to
+ * starts_q, starts_k: device int32 [seqs + 1], ascending (with lengths_k,
+ * starts_k in any order, its last entry unused, and sequences may share keys);
+ * lengths_k: device int32 [seqs] or NULL.  Values that do not fit total_q / total_k are cut to
  * them (no access outside the tensors).
  * max_q bounds the sequences' queries (rows past it are left as they were);
  * max_k only decides how keys are cut into parts, so a wrong one costs time, not
  * correctness.
+ * o         : device, overlaps nothing else.
  * lse       : device fp32 [total_q, heads], contiguous, or NULL.
  * workspace : device, h3a_packed_attention_workspace_size bytes, 16-byte
  *             aligned; NULL when that is 0.  It needs no preparation and holds

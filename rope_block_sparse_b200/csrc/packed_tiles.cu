@@ -6,35 +6,44 @@
 // tile holds T = 128 / group queries (rounded down) of all the group's heads
 // and K and V are loaded once for the whole group.  The tensor map of Q has the
 // group as a dimension, so one TMA box {32 channels, group, 1, T} is one
-// swizzled chunk of such a tile.  One CTA owns two consecutive tiles (2 T
+// swizzled chunk of such a tile.  One CTA owns one or two consecutive tiles (of T
 // queries) of one sequence and kv head and one part of its keys (all of them
-// unless there are too few tiles to fill the GPU).
+// unless there are too few tiles to fill the GPU); packed_plan.cu decides.
 //
 // Which sequence a CTA belongs to is found without a schedule made beforehand:
-// sequence s may use the tile pairs from floor(starts_q[s] / 2T) + s on, which
-// is ascending in s and leaves each sequence at least the ceil(lq / 2T) that it
-// needs; at most `seqs` CTAs find nothing to do.  Later pairs of a sequence see
-// more keys when causal, so CTAs take them in descending order (the longest
-// first).
+// with `span` queries a CTA, sequence s may use the CTAs from floor(starts_q[s] /
+// span) + s on, which is ascending in s and leaves each sequence at least the
+// ceil(lq / span) that it needs; at most `seqs` CTAs find nothing to do.  Later
+// CTAs of a sequence see more keys when causal, so they are taken in descending
+// order (the longest first).  The producer's warp finds the work and starts the first
+// loads while the others set up barriers and TMEM.
 //
 // The pipeline is that of attention.cu (which see for the measurements behind
-// it): warps 0-7 softmax (warpgroup t = tile t, thread = row), warp 8 the TMA
-// producer with K and V rings of 64-byte swizzled chunks, warp 9 QK^T (and, at
-// head_dim 128, PV), warp 10 PV.  S_t = Q_t K^T and O_t += P_t V accumulate in
-// TMEM in fp32; the softmax is online in fp32 against a row reference that
-// moves only when the maximum grew by 2^8; P is rounded to the element type for
-// the PV MMA, whose error (half a step relative a weight) is that of rounding
-// O once more.  What is different:
-//   - the first tile of a pair may need fewer steps than the second (n[0] <=
+// it).  The first four or eight warps are softmax warps (warpgroup t = tile t,
+// thread = row), then come four with a role each: the TMA producer with K and V
+// rings of 64-byte swizzled chunks; the issuer of QK^T (with P over S, of PV too);
+// the issuer of PV where P has a buffer of its own; and the one that looks over V.
+// S_t = Q_t K^T and O_t += P_t V accumulate in TMEM in fp32; the softmax is online
+// in fp32 against a row reference that moves only when the maximum grew by 2^8; P
+// is rounded to the element type for the PV MMA, whose error (half a step relative
+// a weight) is that of rounding O once more.  What is different:
+//   - the first tile of a CTA may need fewer steps than the second (n[0] <=
 //     n[1], causal); it then simply stops earlier;
 //   - every row has its own number of keys; a step whose 128 keys all rows of a
 //     warp attend skips the comparison;
-//   - warp 11 looks over V.  In a step where some row does not attend some key,
-//     a weight of zero times an infinity or NaN in V would be NaN; there it
-//     clears such values in shared memory before PV may read them (the
-//     barrier v_ready) and notes it, and the epilogue adds them back to the rows that
+//   - V is looked over.  In a step where some row does not attend some key, a
+//     weight of zero times an infinity or NaN in V would be NaN; the last warp
+//     clears such values in shared memory before PV may read them (the barrier
+//     v_ready) and notes it, and the epilogue adds them back to the rows that
 //     do attend them.  Only the last one to three steps of a CTA are looked
 //     over; in the others the warp passes the barrier on.
+//
+// What bounds it: long sequences the softmax's exponentials and the tensor core
+// together (two tiles, 128 keys: 2,048 clk of MUFU and at head_dim 128 as many of
+// MMA; one prompt of 16,384, 32/8 heads x 128: 1.75 to 2.03 ms with the power-capped
+// clock, 1.26 to 1.08 PFLOP/s); short ones a CTA's beginning and end, about 4 us (24
+// prompts up to 300, the same heads: 31 us, 8.4 of them HBM's).  A step takes 2,600
+// to 3,000 clk at head_dim 96.
 #include "fastmath.cuh"
 #include "h3a_internal.h"
 #include "half16.cuh"
@@ -118,12 +127,12 @@ struct Smem {
     uint32_t tmem_base;
     int abort_flag;
     int never;      // stays 0: abort flag for waits that must ignore an abort
-    int nonfinite;  // warp 11 cleared a value of V
+    int nonfinite;  // a value of V was cleared
 };
 
 struct TileArgs {
     PackedArgs p;
-    int pairs;     // tile pairs a kv head may have over all sequences
+    int pairs;     // CTAs a kv head may have over all sequences
     int per_tile;  // T: queries of a tile
     int* status;
     uint64_t timeout_ns;
@@ -262,7 +271,7 @@ __device__ void producer(Smem<G>& sm, const TileArgs& a, const Work& w, const CU
         mbar_wait(&sm.v_full[i % G::kStages], (i / G::kStages) & 1u, never, a.timeout_ns);
 }
 
-// Warp 11: passes each V tile on, cleared of infinities and NaN where some row
+// The last warp: passes each V tile on, cleared of infinities and NaN where some row
 // does not attend some key of the step.
 template <class G, bool FP16>
 __device__ void scan_values(Smem<G>& sm, const TileArgs& a, const Work& w, volatile int* abort_flag) {
@@ -443,7 +452,7 @@ __device__ __noinline__ void rescale_o(uint32_t tO, float alpha) {
 }
 
 // Adds the infinities and NaN that 32 channels of V hold among keys [from, to)
-// to o: what warp 11 cleared, for a row that attends those keys.
+// to o: what was cleared, for a row that attends those keys.
 template <bool FP16>
 __device__ __noinline__ void add_nonfinite(float* o, const uint16_t* v, int64_t vn, int from, int to) {
     for (int key = from; key < to; ++key) {
@@ -679,7 +688,7 @@ __device__ void softmax_group(Smem<G>& sm, const TileArgs& a, const Work& w, uin
     uint4* stage = reinterpret_cast<uint4*>(sm.q[t]) + quarter * 32 * (D / 8);
     const int mine = lane * 4, turn = (lane >> 1) & 3;
     auto theirs = [&](int i) { return (i * 8 + lane / 4) * 4 + ((lane & 3) ^ ((lane >> 3) & 3)); };
-    // what warp 11 cleared, for a row that attends it
+    // what was cleared, for a row that attends it
     auto restore = [&](uint32_t* x, int channel) {
         float tmp[32];
 #pragma unroll

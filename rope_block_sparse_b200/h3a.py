@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libh3a (include/h3a.h) over torch tensors.
+"""Thin binding of libh3a (include/h3a.h) over torch tensors: ctypes, and for the
+prompt side's calls, whose kernels take microseconds, compiled (csrc/binding.cpp).
 
 Argument marshalling only: shapes, strides and pointers are read from the
 tensors and passed to the C ABI, which validates them and launches the CUDA
@@ -503,7 +504,7 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts_q
     """Attention over packed sequences with grouped heads: q [total_q, heads, head_dim], k and v [total_k,
     kv_heads, head_dim], bf16 or fp16, head_dim 64, 96 or 128 and contiguous.  Sequence s has the queries
     starts_q[s]:starts_q[s+1] and the keys starts_k[s]:starts_k[s+1], or lengths_k[s] of them from
-    starts_k[s] on (a cache of fixed capacity).  causal: query i of lq attends keys j <= i + lk - lq, so whole
+    starts_k[s] on (a cache's slots, in any order, shared ones too).  causal: query i of lq attends keys j <= i + lk - lq, so whole
     prompts, pieces of prompts and single tokens over a cache are the same call.  max_q and max_k: the
     longest sequence's queries and keys (host numbers).  A query without keys gets zeros.  Returns o, or
     (o, lse) with the natural log-sum-exps, fp32 [total_q, heads]; rows outside every sequence are left as

@@ -120,6 +120,17 @@ def test_padded_cache(lq, d):
 
 
 @pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("lq,used", [([1, 1, 1, 1, 1], [300, 0, 300, 640, 64]), ([1, 4, 2, 3, 1], [9000, 120, 9000, 8999, 1]),
+                                     ([40, 1, 150, 7, 33], [300, 20, 300, 640, 0])], ids=str)
+def test_cache_slots_in_any_order(lq, used, d):
+    """lengths_k: the sequences' slots in any order, one of them read by two sequences."""
+    room = max(used)
+    k, v = randn(room * 4, 2, d, seed=2), randn(room * 4, 2, d, seed=3)
+    slots = [room * i for i in (3, 1, 3, 0, 2)] + [0]
+    check(randn(sum(lq), 8, d, seed=1), k, v, starts(lq), slots, lengths=used)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
 @pytest.mark.parametrize("group", [1, 3, 8])
 @pytest.mark.parametrize("lq,cached", [([150, 200], [0, 40]), ([5, 2], [60, 3]), ([300], [700])], ids=str)
 def test_nonfinite_where_not_attended(lq, cached, group, d):
