@@ -446,8 +446,7 @@ h3a_status h3a_packed_attention_workspace_size(const h3a_packed_desc* d, size_t*
  * multiple of 8 or smaller than what it steps over, an unknown dtype, a scale
  * that is negative or not finite; UNSUPPORTED for head_dim other than 64 / 96 /
  * 128, more than 128 heads to a kv head, total_q, total_k or total_q * heads
- * >= 2^31, strides of 2^39 elements, or a grid beyond 2^31 blocks (65,535 kv heads
- * for more than 16 rows, queries x heads, a kv head); WORKSPACE if it is null,
+ * >= 2^31, strides of 2^39 elements, or a grid beyond 2^31 blocks; WORKSPACE if it is null,
  * misaligned or too small.  A bounded device-side wait that expired is reported by
  * h3a_last_device_error. */
 h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, const h3a_packed_desc* d,

@@ -248,9 +248,7 @@ h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, PackedRoom* 
     const int group = d->heads / d->kv_heads;
     const double columns = plan->tiles ? static_cast<double>(packed_tile_groups(d->total_q, d->seqs, group, plan->tiles))
                                        : std::max(d->seqs, plan->streams);
-    // the tile kernel's grid has the kv heads as its second dimension
-    const double grid = plan->tiles ? (d->kv_heads > 65535 ? static_cast<double>(lim) : columns)
-                                    : columns * d->kv_heads;
+    const double grid = columns * d->kv_heads;
     const double rows = static_cast<double>(d->total_q) * d->heads;
     if (grid >= static_cast<double>(lim) || rows >= static_cast<double>(lim)) return H3A_ERR_UNSUPPORTED;
     *room = PackedRoom{};
