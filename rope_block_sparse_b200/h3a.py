@@ -439,11 +439,19 @@ def rope_plan(rotary_dim: int, theta: float = 10000.0, interleaved: bool = False
     ("none", "linear", "base", "parts": see h3a_rope_scaling), or the given `frequencies` (radians per
     position, rotary_dim / 2 numbers).  interleaved: pairs (2j, 2j+1), else (j, j + rotary_dim/2).
     Host only; plans of the same arguments are made once and shared, so they are not to be written to."""
+    if frequencies is not None:
+        frequencies = tuple(float(f) for f in frequencies)
+    return _rope_plan_as_given(rotary_dim, theta, interleaved, scaling, factor, original_length, low_turns, high_turns,
+                               amplitude, frequencies)
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_plan_as_given(rotary_dim, theta, interleaved, scaling, factor, original_length, low_turns, high_turns,
+                        amplitude, frequencies) -> RopePlan:
     if scaling not in _ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
     return _rope_plan(int(rotary_dim), float(theta), bool(interleaved), scaling, float(factor), int(original_length),
-                      float(low_turns), float(high_turns), float(amplitude),
-                      None if frequencies is None else tuple(float(f) for f in frequencies))
+                      float(low_turns), float(high_turns), float(amplitude), frequencies)
 
 
 @functools.lru_cache(maxsize=64)
