@@ -54,7 +54,7 @@ typedef enum {
     H3A_ERR_UNSUPPORTED = 2, /* head_dim not supported by the call, block != 128, sizes beyond int32 range */
     H3A_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed (see h3a_last_cuda_error_string) */
     H3A_ERR_TIMEOUT = 4,     /* a bounded device-side wait expired; results are undefined */
-    H3A_ERR_WORKSPACE = 5    /* router workspace null or too small */
+    H3A_ERR_WORKSPACE = 5    /* a workspace is null or too small */
 } h3a_status;
 
 /* Token grid of one clip latent: N = T*H*W tokens. */

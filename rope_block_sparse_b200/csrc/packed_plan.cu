@@ -100,12 +100,16 @@ PackedPlan packed_plan(const h3a_packed_desc& d) {
     // Up to 16 rows (queries x heads of a group) fit one mma.m16n8k16 tile of
     // the row kernel, which then reads the keys once; more go to the 128-row
     // tiles of the tcgen05 kernel.
-    // One tile a CTA for short sequences, two for long ones (us, one against two;
-    // 16 prompts): 32/8 heads x 128 up to 300 keys 21.8 / 24.1, 700 51.6 / 53.1, 1,000
-    // 77.9 / 76.8; 28/4 x 96 up to 700 40.3 / 41.1, 1,000 60.5 / 59.2; 16 x 64 up to
-    // 2,000 87.9 / 98.3, but one prompt of 16,000 792 / 771.
-    const int64_t one_tile = d.head_dim == 64 ? 4096 : 768;
-    p.tiles = max_q * group <= kRowSlots ? 0 : max_k <= one_tile ? 1 : 2;
+    // One tile a CTA for short sequences, two for long ones (us, one against two):
+    // 64 prompts, 28/4 heads x 96, up to 250 keys 37.6 / 43.2; 24, 32/8 x 128, up to 300
+    // 29.0 / 29.6; 16 up to 400 26.5 / 25.6, up to 700 47.5 / 43.4; 5, 16 x 128, up to
+    // 350 12.4 / 10.1; 16 x 64: 8 up to 2,000 48.4 / 51.8, one of 6,000 112.7 / 114.9, one
+    // of 16,000 792 / 771.  And one where no sequence's queries fill more: 16 pieces of
+    // up to 8 tokens behind 4,000, 32/8 x 128, 42.4 / 50.3, 32 up to 16 behind 3,000, 28/4
+    // x 96, 27.3 / 32.8.
+    const int64_t one_tile = d.head_dim == 64 ? 8192 : 320;
+    const bool one = max_k <= one_tile || max_q <= packed_queries_per_tile(group);
+    p.tiles = max_q * group <= kRowSlots ? 0 : one ? 1 : 2;
     int64_t splits = 1, chunk = max_k;
     if (p.tiles) {
         splits = tile_splits(d, p.tiles, max_q, max_k);

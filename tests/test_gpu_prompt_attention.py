@@ -73,6 +73,7 @@ PACKS = {
     "single_tokens_16_a_group": ([1] * 3, [700, 64, 2], 32, 2),
     "few_tokens": ([4, 2, 3, 1], [900, 0, 63, 5], 4, 1),
     "chunk_of_a_long_one": ([70], [5000], 4, 2),
+    "one_tile_behind_a_long_one": ([9, 30, 2, 0, 32], [4000, 9000, 100, 70, 3001], 8, 2),
 }
 
 
@@ -151,7 +152,7 @@ def test_nonfinite_where_not_attended(lq, cached, group, d):
     assert o[last].isnan().all()
 
 
-@pytest.mark.parametrize("lq,cached,heads,kv", [([3, 1, 4], [9000, 40, 700], 8, 2), ([130], [9000], 2, 2)], ids=str)
+@pytest.mark.parametrize("lq,cached,heads,kv", [([3, 1, 4], [9000, 40, 700], 8, 2), ([130], [9000], 2, 2), ([30, 9], [9000, 500], 8, 2)], ids=str)
 @pytest.mark.parametrize("d", [64, 96, 128])
 def test_nonfinite_where_not_attended_in_parts(lq, cached, heads, kv, d):
     """The same with keys cut into parts: infinities near the diagonal, NaN in the middle for everyone."""
