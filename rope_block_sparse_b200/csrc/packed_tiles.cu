@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
             fence_barrier_init();
         }
         __syncwarp();
-        early_start();
+        wait_for_previous();
         Work mine;
         mine.none = !find_work(a, G::kTiles, mine);
         if ((threadIdx.x & 31) == 0) {
@@ -809,6 +809,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
     } else if (warp == G::kMmaWarp) {
         tmem_alloc(&sm.tmem_base, G::kTmemCols);
         tmem_relinquish();
+        let_next_start();  // not before: see launch_early
     } else if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sm.s_full[t], 1);
@@ -825,7 +826,7 @@ __global__ void __launch_bounds__(G::kThreads, G::kCtas)
         fence_barrier_init();
     }
     __syncwarp();
-    if (warp != G::kProducerWarp) early_start();
+    if (warp != G::kProducerWarp) wait_for_previous();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();

@@ -20,10 +20,12 @@ constexpr int kSms = 148;  // B200
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // Programmatic dependent launch.  The prompt side's kernels are launched with
-// launch_early and call early_start before they touch global memory: their CTAs
-// may then be set up while the stream's kernel before them still runs, and begin
-// the moment it is complete and its writes are visible.  They let the kernel
-// after them do the same as soon as all their own CTAs have started.
+// launch_early and call early_start, or its two halves, before they touch global
+// memory: their CTAs may then be set up while the stream's kernel before them
+// still runs, and begin the moment it is complete and its writes are visible.
+// They let the kernel after them do the same as soon as all their own CTAs have
+// started; a kernel that allocates TMEM, when all its CTAs have theirs: columns
+// that a CTA of the next launch took first would be held until this launch ends.
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
     cudaLaunchAttribute early{};
@@ -38,9 +40,11 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
     c.numAttrs = 1;
     return cudaLaunchKernelEx(&c, kernel, args...);
 }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void early_start() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next_start();
+    wait_for_previous();
 }
 
 // One-dimensional rotary positions (rope.cu).  A side with heads == 0 is absent.
