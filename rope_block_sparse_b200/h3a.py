@@ -441,22 +441,29 @@ def rope_plan(rotary_dim: int, theta: float = 10000.0, interleaved: bool = False
     Host only; plans of the same arguments are made once and shared, so they are not to be written to."""
     if frequencies is not None:
         frequencies = tuple(float(f) for f in frequencies)
-    return _rope_plan_as_given(rotary_dim, theta, interleaved, scaling, factor, original_length, low_turns, high_turns,
-                               amplitude, frequencies)
+    try:
+        return _rope_plan(rotary_dim, theta, interleaved, scaling, factor, original_length, low_turns, high_turns,
+                          amplitude, frequencies)
+    except (_NotPlain, TypeError):  # a tensor, an array: looked up by the numbers they hold now
+        return _rope_plan(int(rotary_dim), float(theta), bool(interleaved), scaling, float(factor), int(original_length),
+                          float(low_turns), float(high_turns), float(amplitude), frequencies)
 
 
-@functools.lru_cache(maxsize=64)
-def _rope_plan_as_given(rotary_dim, theta, interleaved, scaling, factor, original_length, low_turns, high_turns,
-                        amplitude, frequencies) -> RopePlan:
-    if scaling not in _ROPE_SCALINGS:
-        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
-    return _rope_plan(int(rotary_dim), float(theta), bool(interleaved), scaling, float(factor), int(original_length),
-                      float(low_turns), float(high_turns), float(amplitude), frequencies)
+class _NotPlain(Exception):
+    pass
 
 
 @functools.lru_cache(maxsize=64)
 def _rope_plan(rotary_dim, theta, interleaved, scaling, factor, original_length, low_turns, high_turns, amplitude,
                frequencies) -> RopePlan:
+    """Arguments are looked up as given (0.25 us a call; converting each first takes 1), so only what cannot
+    change is kept: an exception is not."""
+    if not all(isinstance(x, (int, float)) for x in (rotary_dim, theta, interleaved, factor, original_length, low_turns,
+                                                     high_turns, amplitude)):
+        raise _NotPlain
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
+    rotary_dim, interleaved, original_length = int(rotary_dim), bool(interleaved), int(original_length)
     plan = RopePlan()
     if frequencies is not None:
         if len(frequencies) * 2 != rotary_dim:

@@ -1,0 +1,49 @@
+"""rope_plan's arguments, without a GPU: what a plan is made from is the value at the call."""
+import numpy as np
+import pytest
+import torch
+
+from rope_block_sparse_b200 import h3a
+
+
+def turns(plan):
+    return list(plan.turns[:plan.pairs])
+
+
+@pytest.mark.parametrize("name,first,then,kw", [
+    ("theta", 10000.0, 500000.0, {}),
+    ("factor", 2.0, 8.0, dict(scaling="linear")),
+    ("amplitude", 1.0, 1.25, {}),
+    ("original_length", 64, 4096, dict(scaling="parts", factor=4.0)),
+    ("low_turns", 1.0, 2.0, dict(scaling="parts", factor=4.0, original_length=4096)),
+    ("high_turns", 32.0, 8.0, dict(scaling="parts", factor=4.0, original_length=4096)),
+    ("rotary_dim", 64, 32, {}),
+    ("interleaved", False, True, {}),
+])
+def test_a_tensor_written_to_later_gets_its_new_plan(name, first, then, kw):
+    """A number in a 0-d tensor: the same tensor with another value in it is another argument."""
+    kw = {"rotary_dim": 64, **kw}
+    number = torch.tensor(first, dtype=torch.float64 if isinstance(first, float) else None)
+    before = h3a.rope_plan(**{**kw, name: number})
+    number.fill_(then)
+    after = h3a.rope_plan(**{**kw, name: number})
+    for got, value in ((before, first), (after, then)):
+        want = h3a.rope_plan(**{**kw, name: value})
+        assert bytes(got) == bytes(want)
+    assert bytes(before) != bytes(after)
+
+
+def test_numpy_numbers():
+    want = h3a.rope_plan(64, 500000.0, scaling="linear", factor=4.0)
+    assert turns(h3a.rope_plan(np.int64(64), np.float64(500000.0), scaling="linear", factor=np.float32(4.0))) == turns(want)
+    array = np.array(4.0)
+    assert turns(h3a.rope_plan(64, 500000.0, scaling="linear", factor=array)) == turns(want)
+    array[...] = 2.0
+    assert turns(h3a.rope_plan(64, 500000.0, scaling="linear", factor=array)) == turns(h3a.rope_plan(64, 500000.0, scaling="linear", factor=2.0))
+
+
+def test_plans_of_equal_numbers_are_one():
+    """Plain numbers find their plan however they are written, tensors find it by value."""
+    want = h3a.rope_plan(96, 10000.0, scaling="linear", factor=2.0)
+    assert h3a.rope_plan(96, 10000, False, "linear", 2) is want
+    assert h3a.rope_plan(96, 10000, False, "linear", torch.tensor(2.0)) is want
