@@ -501,13 +501,14 @@ def residual_rmsnorm(x: torch.Tensor, f: torch.Tensor | None, gamma: torch.Tenso
     return _binding().residual_rmsnorm(x, f, gamma, eps, code, h, y, s)
 
 
-def packed_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, seqs: int, max_q: int, max_k: int) -> int:
-    """Bytes of workspace packed_attention() needs for these shapes (0: none)."""
+def packed_attention_workspace_size(q: torch.Tensor, k: torch.Tensor, seqs: int, max_q: int, max_k: int,
+                                    causal: bool = True) -> int:
+    """Bytes of workspace packed_attention() needs for these shapes and this `causal` (0: none)."""
     if q.dtype not in _DTYPES:
         raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
     n = ctypes.c_size_t(0)
     d = PackedDesc(_DTYPES[q.dtype], seqs, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], max_q, max_k,
-                   *q.stride()[:2], *k.stride()[:2], *k.stride()[:2], *q.stride()[:2], 1, 0.0)
+                   *q.stride()[:2], *k.stride()[:2], *k.stride()[:2], *q.stride()[:2], bool(causal), 0.0)
     _check("h3a_packed_attention_workspace_size", load().h3a_packed_attention_workspace_size(d, n))
     return n.value
 
