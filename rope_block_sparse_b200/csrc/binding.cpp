@@ -162,6 +162,9 @@ h3a_heads_desc heads_desc(const at::Tensor& x, const at::Tensor& y) {
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 7, [&]() -> PyObject* {
         const at::Tensor &q = tensor(a[0], "q"), &k = maybe(a[1], "k"), &positions = tensor(a[2], "positions");
+        at::Tensor yq = maybe(a[5], "out"), yk = maybe(a[6], "out");
+        const bool given = yq.defined() || yk.defined();
+        require(!given || (yq.defined() && yk.defined() == k.defined()), "out", "must hold a tensor for q, and one for k exactly where k is given");
         const h3a_dtype dtype = check_rows(q, "q", 3);
         const int64_t tokens = q.size(0);
         const int32_t* at_positions = check_index(positions, "positions", tokens, q);
@@ -178,14 +181,10 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         require(fits, "plan", "must be what rope_plan() returns");
         const bool inverse = truth(a[4]);
         const c10::cuda::CUDAGuard guard(q.device());
-        at::Tensor yq = maybe(a[5], "out"), yk = maybe(a[6], "out");
-        if (yk.defined() && !k.defined()) yk = at::Tensor();
-        if (!yq.defined() && !yk.defined()) {
+        if (!given) {
             yq = fresh(q.sizes(), q.scalar_type(), q);
             if (k.defined()) yk = fresh(k.sizes(), q.scalar_type(), q);
         }
-        if (!yq.defined() || k.defined() != yk.defined())
-            throw Refused{"out must hold a tensor for q, and for k where k is given"};
         check_like(yq, "out", 3, q);
         require(yq.sizes() == q.sizes(), "out", "must have the shapes of q and k");
         h3a_heads_desc dq = heads_desc(q, yq), dk{};
@@ -205,14 +204,18 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // residual_rmsnorm(x, f, gamma, eps, scales, h, y, s): scales 0, 1, 2 (h3a_scales);
-// y None for fresh outputs
+// h, y and s all None for fresh outputs
 PyObject* residual_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 8, [&]() -> PyObject* {
         const at::Tensor &x = tensor(a[0], "x"), &f = maybe(a[1], "f"), &gamma = tensor(a[2], "gamma");
+        const int64_t scales = whole(a[4]);
+        at::Tensor h = maybe(a[5], "h"), y = maybe(a[6], "y"), s = maybe(a[7], "scales");
+        const bool given = h.defined() || y.defined() || s.defined();
+        require(!given || (y.defined() && h.defined() == f.defined() && s.defined() == (scales != H3A_SCALES_NONE)), "out",
+                "must hold a tensor for y, for h exactly where f is given and for the scales exactly where y is scaled");
         const h3a_dtype dtype = check_rows(x, "x", 2);
         const int64_t rows = x.size(0), width = x.size(1);
         const float eps = static_cast<float>(number(a[3]));
-        const int64_t scales = whole(a[4]);
         if (f.defined()) {
             check_like(f, "f", 2, x);
             require(f.sizes() == x.sizes(), "f", "must match x");
@@ -223,24 +226,20 @@ PyObject* residual_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const auto y_type = scales == H3A_SCALES_NONE ? x.scalar_type() : at::kFloat8_e4m3fn;
         const int64_t groups = (width + H3A_SCALE_GROUP - 1) / H3A_SCALE_GROUP;
         const c10::cuda::CUDAGuard guard(x.device());
-        at::Tensor h = maybe(a[5], "h"), y = maybe(a[6], "y"), s = maybe(a[7], "scales");
-        if (!f.defined()) h = at::Tensor();
-        if (scales == H3A_SCALES_NONE) s = at::Tensor();
-        if (!y.defined()) {
+        if (!given) {
             if (f.defined()) h = fresh(x.sizes(), x.scalar_type(), x);
             y = fresh(x.sizes(), y_type, x);
             if (scales == H3A_SCALES_ROW) s = fresh({rows}, at::kFloat, x);
             if (scales == H3A_SCALES_GROUP) s = fresh({rows, groups}, at::kFloat, x);
         } else {
             if (f.defined()) {
-                require(h.defined(), "h", "must be given with a residual");
                 check_like(h, "h", 2, x);
                 require(h.sizes() == x.sizes(), "h", "must match x");
             }
             require(y.scalar_type() == y_type && y.sizes() == x.sizes() && (width <= 1 || y.stride(1) == 1) && y.device() == x.device(), "y",
                     "must have x's shape, rows contiguous, and x's type or, with scales, float8_e4m3fn");
             if (scales != H3A_SCALES_NONE)
-                require(s.defined() && s.scalar_type() == at::kFloat && s.is_contiguous() && s.device() == x.device() &&
+                require(s.scalar_type() == at::kFloat && s.is_contiguous() && s.device() == x.device() &&
                             (scales == H3A_SCALES_ROW ? s.dim() == 1 && s.size(0) == rows
                                                       : s.dim() == 2 && s.size(0) == rows && s.size(1) == groups),
                         "scales", "must be a contiguous fp32 [rows] (row) or [rows, ceil(C / 128)] (group) tensor");

@@ -482,7 +482,9 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, plan:
     """One-dimensional rotary positions over bf16 or fp16 q [tokens, heads, head_dim] and k [tokens,
     kv_heads, head_dim] (or None), any strides with head_dim contiguous (slices of a fused QKV buffer).
     positions: int32 [tokens].  inverse rotates back.  Returns (q_out, k_out); inplace=True overwrites
-    q and k, out=(q_out, k_out) writes into given tensors."""
+    q and k, out=(q_out, k_out) writes into given tensors (k_out None where k is)."""
+    if inplace and out is not None:
+        raise ValueError("inplace and out exclude one another")
     q_out, k_out = (q, k) if inplace else (None, None) if out is None else out
     return _binding().rope(q, k, positions, plan, inverse, q_out, k_out)
 
@@ -493,7 +495,7 @@ def residual_rmsnorm(x: torch.Tensor, f: torch.Tensor | None, gamma: torch.Tenso
     (row strides allowed; f None: h = x).  gamma: fp32 [C].  scales None: y in x's type; "row" or
     "group" (128 channels): y in float8_e4m3fn with fp32 scales [rows] or [rows, ceil(C / 128)], so that
     y * scale stands for the normalised row.  Returns (h or None, y, scales or None); out=(h, y, scales)
-    writes into given tensors (h may be x or f)."""
+    writes into given tensors (h may be x or f; None where the call returns None)."""
     code = _SCALES.get(scales)
     if code is None:
         raise ValueError(f'scales must be None, "row" or "group", got {scales!r}')
