@@ -1,7 +1,8 @@
-"""Build libh3a.so in-tree for sm_100a with nvcc, and _binding.so (csrc/binding.cpp)
-against the installed torch with g++.
+"""Build libh3a.so in-tree for sm_100a with nvcc, and where torch is installed its
+binding (csrc/binding.cpp) with g++.
 
     python -m rope_block_sparse_b200.build [--force] [--verbose]
+    python rope_block_sparse_b200/build.py         # the library alone needs no torch
 
 Each .cu file is compiled to an object under ``_build/`` (in parallel), then
 linked into ``rope_block_sparse_b200/libh3a.so`` with the CUDA runtime linked
@@ -38,25 +39,41 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libh3a")
 
 
-def _inputs() -> list:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "h3a.h"))
-    return files
+def _newer(files: list, than: str) -> bool:
+    if not os.path.exists(than):
+        return True
+    t = os.path.getmtime(than)
+    return any(os.path.getmtime(f) > t for f in files)
+
+
+def _library_inputs() -> list:
+    return [os.path.join(INCLUDE, "h3a.h")] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "binding.cpp"]
+
+
+def _binding_inputs() -> list:
+    return [os.path.join(INCLUDE, "h3a.h"), os.path.join(CSRC, "binding.cpp")]
+
+
+def _torch():
+    """The installed torch, or None if there is none with CUDA (one that is broken raises)."""
+    try:
+        import torch
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
+        return None
+    return torch if torch.version.cuda else None
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return _newer(_library_inputs(), LIB) or (_torch() is not None and _newer(_binding_inputs(), BINDING))
 
 
 def _binding_cmd(out: str) -> list:
     """g++ of the torch binding; it finds libh3a.so beside itself."""
     import sysconfig
 
-    import torch
-
+    torch = _torch()
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     includes = [os.path.join(root, "include"), sysconfig.get_paths()["include"], cuda]
@@ -68,8 +85,19 @@ def _binding_cmd(out: str) -> list:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not needs_build():
-        return LIB
+    """Builds what is not up to date; without torch the library alone, whose C ABI does not need it."""
+    if force or _newer(_library_inputs(), LIB):
+        _build_library(verbose)
+    if _torch() is None:
+        print("no torch with CUDA: libh3a.so is built, its torch binding is not", file=sys.stderr)
+    elif force or _newer(_binding_inputs(), BINDING):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        subprocess.check_call(_binding_cmd(tmp))
+        os.replace(tmp, BINDING)
+    return LIB
+
+
+def _build_library(verbose: bool) -> None:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     procs = []
@@ -92,10 +120,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     link = [nvcc, *ARCH, "-shared", "-o", tmp, "-Xlinker", "-soname=libh3a.so", *[o for _, o, _, _ in procs], "-cudart", "static"]
     subprocess.check_call(link)
     os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    subprocess.check_call(_binding_cmd(tmp))
-    os.replace(tmp, BINDING)
-    return LIB
 
 
 if __name__ == "__main__":
