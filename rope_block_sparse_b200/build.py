@@ -24,7 +24,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libh3a.so")
-BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["h3a_api.cu", "prologue.cu", "router.cu", "attention.cu", "selftest.cu", "route_noalloc.cu", "dit_ops.cu",
            "rope.cu", "rmsnorm.cu", "packed_plan.cu", "packed_tiles.cu", "packed_rows.cu", "packed_combine.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -65,15 +64,22 @@ def _torch():
     return torch if torch.version.cuda else None
 
 
+def binding_path(torch) -> str:
+    """The binding for this torch and Python.  It uses torch's C++ classes and Python's API as they were when it
+    was compiled, so its name says which, as an extension module's does, and no other is loaded or kept."""
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(PKG, f"_binding.torch-{torch.__version__}.abi{abi}.{sys.implementation.cache_tag}.so")
+
+
 def needs_build() -> bool:
-    return _newer(_library_inputs(), LIB) or (_torch() is not None and _newer(_binding_inputs(), BINDING))
+    torch = _torch()
+    return _newer(_library_inputs(), LIB) or (torch is not None and _newer(_binding_inputs(), binding_path(torch)))
 
 
-def _binding_cmd(out: str) -> list:
+def _binding_cmd(torch, out: str) -> list:
     """g++ of the torch binding; it finds libh3a.so beside itself."""
     import sysconfig
 
-    torch = _torch()
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     includes = [os.path.join(root, "include"), sysconfig.get_paths()["include"], cuda]
@@ -88,12 +94,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Builds what is not up to date; without torch the library alone, whose C ABI does not need it."""
     if force or _newer(_library_inputs(), LIB):
         _build_library(verbose)
-    if _torch() is None:
+    torch = _torch()
+    if torch is None:
         print("no torch with CUDA: libh3a.so is built, its torch binding is not", file=sys.stderr)
-    elif force or _newer(_binding_inputs(), BINDING):
-        tmp = BINDING + f".tmp{os.getpid()}"
-        subprocess.check_call(_binding_cmd(tmp))
-        os.replace(tmp, BINDING)
+    elif force or _newer(_binding_inputs(), binding_path(torch)):
+        tmp = binding_path(torch) + f".tmp{os.getpid()}"
+        subprocess.check_call(_binding_cmd(torch, tmp))
+        os.replace(tmp, binding_path(torch))
     return LIB
 
 

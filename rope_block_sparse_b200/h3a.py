@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 
 import torch
@@ -424,10 +425,16 @@ SCALE_GROUP = 128  # H3A_SCALE_GROUP
 
 @functools.cache
 def _binding():
-    """The compiled binding of the prompt side's calls (csrc/binding.cpp; raises if it was not built)."""
-    load()
-    from . import _binding as module
+    """The compiled binding of the prompt side's calls (csrc/binding.cpp; raises if it was not built for this torch)."""
+    from .build import binding_path
 
+    load()
+    path = binding_path(torch)
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} not found; build it for this torch and Python with `python -m rope_block_sparse_b200.build`")
+    spec = importlib.util.spec_from_file_location(f"{__package__}._binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
     module.set_error(H3AError)
     return module
 
