@@ -452,7 +452,7 @@ def rope_plan(rotary_dim: int, theta: float = 10000.0, interleaved: bool = False
         return _rope_plan(rotary_dim, theta, interleaved, scaling, factor, original_length, low_turns, high_turns,
                           amplitude, frequencies)
     except (_NotPlain, TypeError):  # a tensor, an array: looked up by the numbers they hold now
-        return _rope_plan(int(rotary_dim), float(theta), bool(interleaved), scaling, float(factor), int(original_length),
+        return _rope_plan(float(rotary_dim), float(theta), bool(interleaved), scaling, float(factor), float(original_length),
                           float(low_turns), float(high_turns), float(amplitude), frequencies)
 
 
@@ -470,6 +470,9 @@ def _rope_plan(rotary_dim, theta, interleaved, scaling, factor, original_length,
         raise _NotPlain
     if scaling not in _ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
+    for name, x, most in (("rotary_dim", rotary_dim, 2 ** 31), ("original_length", original_length, 2 ** 63)):
+        if not -most <= x < most or x != int(x):
+            raise ValueError(f"{name} must be a whole number, got {x}")
     rotary_dim, interleaved, original_length = int(rotary_dim), bool(interleaved), int(original_length)
     plan = RopePlan()
     if frequencies is not None:

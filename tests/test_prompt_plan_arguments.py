@@ -47,3 +47,18 @@ def test_plans_of_equal_numbers_are_one():
     want = h3a.rope_plan(96, 10000.0, scaling="linear", factor=2.0)
     assert h3a.rope_plan(96, 10000, False, "linear", 2) is want
     assert h3a.rope_plan(96, 10000, False, "linear", torch.tensor(2.0)) is want
+
+
+@pytest.mark.parametrize("kw", [dict(rotary_dim=64.7), dict(rotary_dim=torch.tensor(64.5)), dict(rotary_dim=float("nan")), dict(rotary_dim=float("inf")),
+                                dict(rotary_dim=2 ** 32 + 64), dict(rotary_dim=64, scaling="parts", original_length=100.5),
+                                dict(rotary_dim=64, scaling="parts", original_length=2 ** 64 + 100)], ids=str)
+def test_numbers_that_are_not_whole_are_refused(kw):
+    """Neither cut to a whole number nor to the C call's type."""
+    with pytest.raises(ValueError, match=next(n for n in ("original_length", "rotary_dim") if n in kw)):
+        h3a.rope_plan(**kw)
+
+
+def test_whole_numbers_in_any_form():
+    want = h3a.rope_plan(64, scaling="parts", factor=2.0, original_length=4096)
+    for r, n in ((64.0, 4096.0), (torch.tensor(64), torch.tensor(4096.0)), (np.int32(64), np.float32(4096))):
+        assert bytes(h3a.rope_plan(r, scaling="parts", factor=2.0, original_length=n)) == bytes(want)
