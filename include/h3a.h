@@ -329,8 +329,9 @@ typedef enum { H3A_ROPE_PLAIN = 0, H3A_ROPE_LINEAR = 1, H3A_ROPE_BASE = 2, H3A_R
  * low_turns and high_turns are read for H3A_ROPE_PARTS only.
  * Errors: INVALID_ARG for a null plan, an odd or non-positive rotary_dim,
  * theta <= 0, factor <= 0, an unknown scaling, original_length < 1 or
- * high_turns <= low_turns with H3A_ROPE_PARTS, or a value that is not finite;
- * UNSUPPORTED for rotary_dim > 256. */
+ * high_turns <= low_turns with H3A_ROPE_PARTS, or a value that is not finite (the
+ * amplitude in fp32, the stretched base, the frequencies); UNSUPPORTED for
+ * rotary_dim > 256. */
 h3a_status h3a_rope_plan_scaled(int32_t rotary_dim, int32_t interleaved, double theta, h3a_rope_scaling scaling,
                                 double factor, int64_t original_length, double low_turns, double high_turns,
                                 double amplitude, h3a_rope_plan* plan);

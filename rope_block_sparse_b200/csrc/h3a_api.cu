@@ -211,7 +211,7 @@ bool strides_ok(int64_t sn, int64_t sh, int64_t rows, int64_t heads, int64_t d) 
 }
 
 h3a_status rope_plan_check(int32_t rotary_dim, const h3a_rope_plan* plan, double amplitude) {
-    if (!plan || rotary_dim < 2 || rotary_dim % 2 || !std::isfinite(amplitude)) return H3A_ERR_INVALID_ARG;
+    if (!plan || rotary_dim < 2 || rotary_dim % 2 || !std::isfinite(static_cast<float>(amplitude))) return H3A_ERR_INVALID_ARG;
     return rotary_dim > 2 * H3A_ROPE_MAX_PAIRS ? H3A_ERR_UNSUPPORTED : H3A_OK;
 }
 
@@ -488,6 +488,7 @@ h3a_status h3a_rope_plan_scaled(int32_t rotary_dim, int32_t interleaved, double 
         return H3A_ERR_INVALID_ARG;
     const double r = rotary_dim;
     if (scaling == H3A_ROPE_BASE && rotary_dim > 2) theta *= std::pow(factor, r / (r - 2.0));
+    if (!std::isfinite(theta)) return H3A_ERR_INVALID_ARG;
     double f[H3A_ROPE_MAX_PAIRS];
     for (int j = 0; j < rotary_dim / 2; ++j) {
         f[j] = std::pow(theta, -2.0 * j / r);

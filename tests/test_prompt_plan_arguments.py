@@ -62,3 +62,11 @@ def test_whole_numbers_in_any_form():
     want = h3a.rope_plan(64, scaling="parts", factor=2.0, original_length=4096)
     for r, n in ((64.0, 4096.0), (torch.tensor(64), torch.tensor(4096.0)), (np.int32(64), np.float32(4096))):
         assert bytes(h3a.rope_plan(r, scaling="parts", factor=2.0, original_length=n)) == bytes(want)
+
+
+@pytest.mark.parametrize("kw", [dict(amplitude=1e39), dict(amplitude=-1e300), dict(scaling="base", theta=1e300, factor=1e300),
+                                dict(frequencies=[0.5] * 32, amplitude=1e39)], ids=str)
+def test_numbers_that_are_infinite_in_the_plan_are_refused(kw):
+    """Finite as given, but the amplitude is kept in 32 bits, and a stretched base may leave 64."""
+    with pytest.raises(h3a.H3AError, match="INVALID_ARG"):
+        h3a.rope_plan(64, **kw)
