@@ -445,10 +445,11 @@ h3a_status h3a_packed_attention_workspace_size(const h3a_packed_desc* d, size_t*
  * Errors: INVALID_ARG for null or misaligned pointers, seqs < 1, heads no
  * positive multiple of kv_heads, negative sizes, max_q or max_k < 0, a stride no
  * multiple of 8 or smaller than what it steps over, an unknown dtype, a scale
- * that is negative or not finite; UNSUPPORTED for head_dim other than 64 / 96 /
- * 128, more than 128 heads to a kv head, total_q, total_k or total_q * heads
- * >= 2^31, strides of 2^39 elements, or a grid beyond 2^31 blocks; WORKSPACE if it is null,
- * misaligned or too small.  A bounded device-side wait that expired is reported by
+ * that is negative or, times log2 e, not finite in fp32; UNSUPPORTED for
+ * head_dim other than 64 / 96 / 128, more than 128 heads to a kv head, total_q,
+ * total_k or total_q * heads >= 2^31, strides of 2^39 elements, or a grid beyond
+ * 2^31 blocks; WORKSPACE if it is null, misaligned or too small.  A bounded
+ * device-side wait that expired is reported by
  * h3a_last_device_error. */
 h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, const h3a_packed_desc* d,
                                 const int32_t* starts_q, const int32_t* starts_k, const int32_t* lengths_k, void* o,

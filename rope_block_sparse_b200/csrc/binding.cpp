@@ -98,6 +98,13 @@ double number(PyObject* o) {
     if (v == -1.0 && PyErr_Occurred()) throw Refused{""};
     return v;
 }
+// As fp32; what fp32 rounds to zero is not meant as the zero that turns a number off.
+float number32(PyObject* o, const char* name) {
+    const double v = number(o);
+    const float f = static_cast<float>(v);
+    require(f != 0.0f || v == 0.0, name, "is so small that it would be zero in fp32");
+    return f;
+}
 int64_t whole(PyObject* o) {
     PyObject* i = PyNumber_Index(o);  // no fractions
     if (i == nullptr) throw Refused{""};
@@ -208,6 +215,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* residual_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 8, [&]() -> PyObject* {
         const at::Tensor &x = tensor(a[0], "x"), &f = maybe(a[1], "f"), &gamma = tensor(a[2], "gamma");
+        const float eps = static_cast<float>(number(a[3]));
         const int64_t scales = whole(a[4]);
         at::Tensor h = maybe(a[5], "h"), y = maybe(a[6], "y"), s = maybe(a[7], "scales");
         const bool given = h.defined() || y.defined() || s.defined();
@@ -215,7 +223,6 @@ PyObject* residual_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 "must hold a tensor for y, for h exactly where f is given and for the scales exactly where y is scaled");
         const h3a_dtype dtype = check_rows(x, "x", 2);
         const int64_t rows = x.size(0), width = x.size(1);
-        const float eps = static_cast<float>(number(a[3]));
         if (f.defined()) {
             check_like(f, "f", 2, x);
             require(f.sizes() == x.sizes(), "f", "must match x");
@@ -264,6 +271,7 @@ PyObject* packed_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
         const at::Tensor &starts_q = tensor(a[3], "starts_q"), &starts_k = tensor(a[4], "starts_k"), &lengths = maybe(a[7], "lengths_k");
         h3a_packed_desc d{};
+        d.scale = number32(a[9], "scale");
         d.dtype = check_rows(q, "q", 3);
         check_like(k, "k", 3, q);
         check_like(v, "v", 3, q);
@@ -274,7 +282,6 @@ PyObject* packed_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int32_t* lk = lengths.defined() ? check_index(lengths, "lengths_k", seqs, q) : nullptr;
         d.max_q = whole(a[5]), d.max_k = whole(a[6]);
         d.causal = truth(a[8]);
-        d.scale = static_cast<float>(number(a[9]));
         const bool with_lse = truth(a[10]);
         const c10::cuda::CUDAGuard guard(q.device());
         at::Tensor workspace = maybe(a[11], "workspace"), out = maybe(a[12], "out"), lse;

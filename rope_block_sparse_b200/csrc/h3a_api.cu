@@ -222,6 +222,12 @@ uint64_t turns_of(double frequency) {
     return static_cast<uint64_t>(std::fmod(std::ldexp(part, 64), 18446744073709551616.0));
 }
 
+// The logit scale in the kernels' log2 units.
+float packed_scale_log2(const h3a_packed_desc& d) {
+    const double scale = d.scale == 0.0f ? 1.0 / std::sqrt(static_cast<double>(d.head_dim)) : d.scale;
+    return static_cast<float>(scale * 1.4426950408889634);
+}
+
 // Checks a packed descriptor and lays out its partial rows.
 struct PackedRoom {
     size_t o, lse, all;  // bytes of the partial rows, up to their log-sum-exps' end, and of everything
@@ -230,7 +236,7 @@ h3a_status packed_check(const h3a_packed_desc* d, PackedPlan* plan, PackedRoom* 
     if (d == nullptr || !known(d->dtype)) return H3A_ERR_INVALID_ARG;
     if (d->seqs < 1 || d->heads < 1 || d->kv_heads < 1 || d->heads % d->kv_heads) return H3A_ERR_INVALID_ARG;
     if (d->total_q < 0 || d->total_k < 0 || d->max_q < 0 || d->max_k < 0) return H3A_ERR_INVALID_ARG;
-    if (!(d->scale >= 0.0f) || !std::isfinite(d->scale)) return H3A_ERR_INVALID_ARG;
+    if (!(d->scale >= 0.0f) || (d->scale > 0.0f && !std::isfinite(packed_scale_log2(*d)))) return H3A_ERR_INVALID_ARG;
     if (d->head_dim != 64 && d->head_dim != 96 && d->head_dim != 128) return H3A_ERR_UNSUPPORTED;
     if (d->heads / d->kv_heads > 128) return H3A_ERR_UNSUPPORTED;
     const int64_t lim = int64_t(1) << 31;
@@ -587,8 +593,7 @@ h3a_status h3a_packed_attention(const void* q, const void* k, const void* v, con
     a.total_q = d->total_q, a.total_k = d->total_k, a.max_q = d->max_q;
     a.seqs = d->seqs, a.heads = d->heads, a.kv_heads = d->kv_heads, a.group = d->heads / d->kv_heads;
     a.causal = d->causal != 0;
-    const double scale = d->scale == 0.0f ? 1.0 / std::sqrt(static_cast<double>(d->head_dim)) : d->scale;
-    a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    a.scale_log2 = packed_scale_log2(*d);
     a.splits = plan.splits, a.chunk = plan.chunk, a.streams = plan.streams;
     if (room.all > 0) {
         a.part_o = static_cast<float*>(workspace);
