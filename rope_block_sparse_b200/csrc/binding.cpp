@@ -215,7 +215,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* residual_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 8, [&]() -> PyObject* {
         const at::Tensor &x = tensor(a[0], "x"), &f = maybe(a[1], "f"), &gamma = tensor(a[2], "gamma");
-        const float eps = static_cast<float>(number(a[3]));
+        const float eps = number32(a[3], "eps");
         const int64_t scales = whole(a[4]);
         at::Tensor h = maybe(a[5], "h"), y = maybe(a[6], "y"), s = maybe(a[7], "scales");
         const bool given = h.defined() || y.defined() || s.defined();

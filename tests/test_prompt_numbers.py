@@ -16,6 +16,12 @@ def test_a_scale_that_would_select_the_default(scale, match):
         h3a.packed_attention(Q, Q, Q, I, I, 4, 4, scale=scale)
 
 
+@pytest.mark.parametrize("eps,match", [(1e-60, "eps"), (0.0, "CUDA"), (1e-30, "CUDA"), (1e-6, "CUDA")])
+def test_an_eps_that_would_be_none(eps, match):
+    with pytest.raises(ValueError, match=match):
+        h3a.residual_rmsnorm(Q[:, 0], None, torch.ones(64), eps)
+
+
 @NO_GPU
 def test_a_scale_that_is_infinite_in_the_kernels_units():
     """Logits are kept times log2 e: 2^127.6 is finite and that is not."""
