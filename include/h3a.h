@@ -371,11 +371,17 @@ typedef enum { H3A_SCALES_NONE = 0, H3A_SCALES_ROW = 1, H3A_SCALES_GROUP = 2 } h
 /* The residual's addition and the root-mean-square norm, one pass over device
  * memory (the prompt side's counterpart of h3a_residual_adaln).  For every row:
  *   h = x + f, rounded once to the element type (f == NULL: h = x)
- *   y = h / sqrt(mean(h^2) + eps) * gamma     (statistics of the rounded h, fp32)
+ *   y = h / sqrt(mean(h^2) + eps) * gamma     (statistics of the rounded h, fp32:
+ *       the sum of h^2 has to stay in fp32's range.  Beyond it, |h| of about 1e17, y
+ *       is 0; with eps = 0 and all |h| under about 1e-19 y loses its accuracy, and
+ *       under 1e-23 it is infinite or NaN)
  * H3A_SCALES_NONE: y rounded once to the element type.  Otherwise, per row or
  * per group of 128 channels (the last group may be shorter):
  *   scale = max(max|y|, 2^-100) / 448, y8 = e4m3(y / scale) (nearest even),
- * so that y8 * scale stands for y; a NaN makes its scale NaN.
+ * so that y8 * scale stands for y; a NaN makes its scale NaN.  Both divisions are
+ * products with the fp32 reciprocal, so scale and y / scale are within a few
+ * roundings of 2^-24 of the quotients, and a y / scale that close to the middle
+ * between two codes may take either.
  * x, f, h_out : device, [rows, width] with row strides; f may be NULL.  h_out
  *               is written when f != NULL (then required; may be x or f with
  *               the same stride).

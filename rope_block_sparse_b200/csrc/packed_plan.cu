@@ -106,7 +106,8 @@ PackedPlan packed_plan(const h3a_packed_desc& d) {
     // 350 12.4 / 10.1; 16 x 64: 8 up to 2,000 48.4 / 51.8, one of 6,000 112.7 / 114.9, one
     // of 16,000 792 / 771.  And one where no sequence's queries fill more: 16 pieces of
     // up to 8 tokens behind 4,000, 32/8 x 128, 42.4 / 50.3, 32 up to 16 behind 3,000, 28/4
-    // x 96, 27.3 / 32.8.
+    // x 96, 27.3 / 32.8.  The 320 keys come from head_dim 128; at 96, whose two-tile form has
+    // a P buffer of its own, the figures above are all there is.
     const int64_t one_tile = d.head_dim == 64 ? 8192 : 320;
     const bool one = max_k <= one_tile || max_q <= packed_queries_per_tile(group);
     p.tiles = max_q * group <= kRowSlots ? 0 : one ? 1 : 2;

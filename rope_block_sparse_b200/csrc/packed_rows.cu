@@ -23,9 +23,10 @@
 // their rows of a key lie behind one another in memory, and apart in time they
 // are 256 bytes here and there (16,000 keys of 8 kv heads x 128 by stretches of
 // single heads: 20.5 us, side by side 16).  Measured, with the joining: 47 caches of
-// up to 16,384 keys, 32/8 heads x 128, 1.11 GB: 177 to 184 us, 6.0 to 6.3 TB/s = 0.92
-// to 0.96 of a copy; 8 of up to 900, 16 heads x 64: 7.6 us, bound by latency (1.3 us of
-// HBM).
+// up to 16,384 keys, 32/8 heads x 128, 1.11 GB: 176 to 188 us, 5.9 to 6.3 TB/s = 0.90
+// to 0.96 of a copy; 8 of up to 900, 16 heads x 64: 7.6 to 8.4 us, of which HBM takes 1.3 and
+// a launch 1.6 to 2.0; what the others go to is not known (more units on their way did not
+// shorten it).
 //
 // Keys no row attends are read as zeros (cp.async with a source size of 0), so
 // what lies behind a sequence is never touched.  Where some rows attend a key

@@ -43,10 +43,10 @@
 //
 // What bounds it: long sequences the softmax's exponentials and the tensor core
 // together (two tiles, 128 keys: 2,048 clk of MUFU and at head_dim 128 as many of
-// MMA; one prompt of 16,384, 32/8 heads x 128: 1.75 to 2.03 ms with the power-capped
-// clock, 1.26 to 1.08 PFLOP/s); short ones a CTA's beginning and end, about 4 us (24
-// prompts up to 300, the same heads: 29 us, 8.4 of them HBM's).  A step takes 2,600
-// to 3,000 clk at head_dim 96.
+// MMA; one prompt of 16,384, 32/8 heads x 128: 2.0 ms at the clock that
+// the power cap leaves, 1.08 PFLOP/s; 1.75 ms before the cap takes hold); short
+// ones a CTA's beginning and end, about 4 us (24 prompts up to 300, the same
+// heads: 29 us, 8.4 of them HBM's).  A step takes 2,600 to 3,000 clk at head_dim 96.
 #include "fastmath.cuh"
 #include "h3a_internal.h"
 #include "half16.cuh"

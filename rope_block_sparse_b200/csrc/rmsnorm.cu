@@ -16,7 +16,9 @@
 // and 24 through shared memory, 8,000 of 8,192 without 49 and 43, but 8,192 of
 // 4,096 with it 39.7 and 42.)  The sum of squares and max|h * gamma| are reduced
 // together (one barrier a row, none for parts of a warp); max|y| is r times the
-// latter.  Divisions are taken once a row or group, as reciprocals.
+// latter.  Divisions are taken once a row or group, as reciprocals: y / scale is then two
+// roundings from the quotient instead of one, 2^-24 against e4m3's 2^-4, and a value on
+// the border of two codes may take the other one.
 // Measured: 124,992 rows of 5,376 with residual and row scales 784 us (4.70 GB,
 // 6.0 TB/s = 0.91 of a copy), 8,192 of 4,096 with group scales 40.6 us (0.89).
 #include <algorithm>

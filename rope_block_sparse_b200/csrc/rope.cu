@@ -91,9 +91,11 @@ __host__ __device__ __forceinline__ int rotated_slots(int pairs) {
 __device__ __forceinline__ int angle_at(int slot, int e, int rotated) { return ((e >> 1) * rotated + slot) * 2 + (e & 1); }
 
 // Blocks in flight and queued per multiprocessor.  8,192 tokens of 40 heads x 128:
-// 31.5 us at 8, 28.8 at 16, 27.6 at 32 (one chunk each then; 168 MB, 6.1 TB/s =
-// 0.93 of a copy).  30,011 tokens of 32 heads x 96, half rotated: 58.3 us (369
-// MB, 6.3 TB/s).  Angles per thread instead of per chunk took 37 and 97 us.
+// 31.5 us at 8, 28.8 at 16, 27.6 at 32 (one chunk each then); as it stands 26.9 (168
+// MB, 6.2 TB/s = 0.95 of a copy).  30,011 tokens of 32 heads x 96, half rotated: 57.1 us
+// (369 MB, 6.5 TB/s).  Angles per thread instead of per chunk took 37 and 97 us.  The
+// same 8,192 tokens with 25 rotated pairs: 31.9 us as neighbours, 40.8 as halves
+// (kHalvesAny: eight 2-byte shared loads a vector), 43.2 with 63 pairs.
 constexpr int kBlocksPerSm = 32;
 constexpr int kThreads = 128;
 
