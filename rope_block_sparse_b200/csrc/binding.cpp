@@ -2,8 +2,9 @@
 // checks, fresh outputs, the tensors' device and its current stream, then the
 // C ABI.  A single-token step's kernels take two to ten microseconds; the same
 // work in Python and ctypes took the host 14 to 19 a call, here it takes 3.9 to
-// 4.6 (packed_attention) and 5.1 (rope, residual_rmsnorm).  Every function is positional and returns new or given tensors; wrong
-// arguments raise ValueError, a status other than H3A_OK the H3AError of h3a.py.
+// 4.6 (packed_attention) and 5.1 (rope, residual_rmsnorm).  Every function is
+// positional and returns new or given tensors; wrong arguments raise ValueError, a
+// status other than H3A_OK the H3AError of h3a.py.
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
